@@ -16,14 +16,18 @@ from .binding import (  # noqa: F401
     FaError,
     attention_backward,
     attention_backward_varlen,
+    attention_backward_varlen_gqa,
     attention_decode_paged,
     attention_forward,
     attention_forward_fp8,
     attention_forward_varlen,
+    attention_forward_varlen_gqa,
     fa_bwd,
     fa_bwd_deterministic,
     fa_bwd_varlen,
     fa_bwd_varlen_deterministic,
+    fa_bwd_varlen_gqa,
+    fa_bwd_varlen_gqa_deterministic,
     fa_bwd_workspace_size,
     fa_check_status,
     fa_decode_paged,
@@ -31,6 +35,7 @@ from .binding import (  # noqa: F401
     fa_fwd,
     fa_fwd_fp8,
     fa_fwd_varlen,
+    fa_fwd_varlen_gqa,
     fa_quantize_fp8,
     fa_status_string,
     library_path,

@@ -43,6 +43,9 @@ SIGNATURES = {
                                   ctypes.c_size_t, _P]),
     "fa_bwd_varlen_deterministic": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                                          _F, _I, _P, ctypes.c_size_t, _P]),
+    "fa_fwd_varlen_gqa": (_I, [_P] * 7 + [_I] * 8 + [_F, _I, _P]),
+    "fa_bwd_varlen_gqa": (_I, [_P] * 11 + [_I] * 8 + [_F, _I, _P, ctypes.c_size_t, _P]),
+    "fa_bwd_varlen_gqa_deterministic": (_I, [_P] * 11 + [_I] * 8 + [_F, _I, _P, ctypes.c_size_t, _P]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_last_cuda_error": (ctypes.c_char_p, []),
@@ -219,6 +222,120 @@ def attention_backward_varlen(q, k, v, o, lse, dO, cu_seqlens_q, cu_seqlens_k, m
     import torch
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fn = fa_bwd_varlen_deterministic if deterministic else fa_bwd_varlen
+    fn(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
+       workspace, stream)
+    return dq, dk, dv
+
+
+def _on_device(where, first, *tensors):
+    """The device of a call whose tensors must all live on it."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{where} needs CUDA tensors")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+    return dev
+
+
+def _call(where, dev, stream, *args):
+    """Calls the C entry point ``where`` with ``dev`` current, on ``stream``
+    (None: the current stream of ``dev``) as its last argument."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {dev}")
+    fn = getattr(load_library(), where)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def _check_gqa(where, q, k, v, q_like, k_like, lse, cu_seqlens_q, cu_seqlens_k):
+    """Shapes of a grouped-head packed call: (device, the C call's sizes up to total_k)."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_thd(name, t)
+    (total_q, H, d), (total_k, H_kv, _) = q.shape, k.shape
+    for like, ts in ((q, q_like), (k, (("v", v),) + k_like)):
+        for name, t in ts:
+            _check_thd(name, t)
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    if k.shape[2] != d or H_kv < 1 or H % H_kv:
+        raise ValueError("k and v must have q's head dim and a number of heads that divides q's")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [H, total_q] CUDA tensor")
+    _check_cu("cu_seqlens_q", cu_seqlens_q)
+    batch = cu_seqlens_q.numel() - 1
+    _check_cu("cu_seqlens_k", cu_seqlens_k, batch)
+    if not cu_seqlens_q.is_contiguous() or not cu_seqlens_k.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous")
+    dev = _on_device(where, q, k, v, lse, cu_seqlens_q, cu_seqlens_k, *(t for _, t in q_like + k_like))
+    return dev, (batch, H, H_kv, d, total_q, total_k)
+
+
+def fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
+                      scale: float, causal: bool, stream=None) -> None:
+    """Packed forward with grouped heads (q [total_q, H, d], k and v
+    [total_k, H_kv, d]); same semantics as the C entry point."""
+    dev, sizes = _check_gqa("fa_fwd_varlen_gqa", q, k, v, (("o", o),), (), lse, cu_seqlens_q, cu_seqlens_k)
+    _call("fa_fwd_varlen_gqa", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q),
+          _ptr(cu_seqlens_k), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)))
+
+
+def attention_forward_varlen_gqa(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
+                                 stream=None):
+    """Allocates O [total_q, H, d] and LSE [H, total_q], then calls fa_fwd_varlen_gqa."""
+    import torch
+    o = torch.empty_like(q)
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal, stream)
+    return o, lse
+
+
+def _bwd_varlen_gqa(fn, q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                    scale, causal, workspace, stream) -> None:
+    import torch
+    dev, sizes = _check_gqa(fn, q, k, v, (("o", o), ("dO", dO), ("dq", dq)), (("dk", dk), ("dv", dv)), lse,
+                            cu_seqlens_q, cu_seqlens_k)
+    if workspace is None:
+        need = fa_bwd_workspace_size(sizes[0], sizes[1], int(max_seqlen_q), sizes[3])
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _on_device(fn, q, workspace)
+    _call(fn, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
+          _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale),
+          int(bool(causal)), _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def fa_bwd_varlen_gqa(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                      max_seqlen_k: int, scale: float, causal: bool, workspace=None, stream=None) -> None:
+    """Packed backward with grouped heads; same semantics as the C entry point."""
+    _bwd_varlen_gqa("fa_bwd_varlen_gqa", q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                    max_seqlen_k, scale, causal, workspace, stream)
+
+
+def fa_bwd_varlen_gqa_deterministic(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                                    max_seqlen_k: int, scale: float, causal: bool, workspace=None,
+                                    stream=None) -> None:
+    """fa_bwd_varlen_gqa with dQ summed in a fixed order: bitwise reproducible results."""
+    _bwd_varlen_gqa("fa_bwd_varlen_gqa_deterministic", q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k,
+                    max_seqlen_q, max_seqlen_k, scale, causal, workspace, stream)
+
+
+def attention_backward_varlen_gqa(q, k, v, o, lse, dO, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                  scale, causal, workspace=None, stream=None, deterministic: bool = False):
+    """Allocates dQ, dK, dV, then calls fa_bwd_varlen_gqa (or its deterministic
+    form). Returns (dQ, dK, dV)."""
+    import torch
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fn = fa_bwd_varlen_gqa_deterministic if deterministic else fa_bwd_varlen_gqa
     fn(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
        workspace, stream)
     return dq, dk, dv

@@ -1,5 +1,6 @@
 // C ABI of the attention library: argument checks, TMA tensor-map encoding and
 // kernel launches on the caller's stream. No device memory is allocated here.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -123,6 +124,24 @@ bool encode_thd(CUtensorMap* m, const void* ptr, int H, int total, int D, int bo
   return encode_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The same for a grouped Q tile: box = 64 columns x P heads x tok tokens (in
+// shared memory row token * P + head).
+bool encode_thd_group(CUtensorMap* m, const void* ptr, int H, int total, int D, fa::QTile t) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H), static_cast<uint64_t>(total)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(H) * D * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(t.P), static_cast<uint32_t>(t.tok)};
+  return encode_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Heads packed into one Q tile for groups of G heads: the largest divisor P of
+// G that leaves at most 4 of the tile's 128 rows unused (128 / P whole tokens;
+// a P of 24 or 48 would waste 8 or 32 rows in every tile of a long prompt).
+fa::QTile q_tile(int G) {
+  int P = std::min(G, 128);
+  while (G % P != 0 || 128 / P * P < 124) --P;  // P = 1 always fits
+  return fa::QTile{P, 128 / P};
+}
+
 // 3-D map over an 8-bit tensor [dim2][dim1][dim0] (dim0 contiguous, row
 // pitch stride1 bytes, slice pitch stride2 bytes); box = 128 x 128 x 1 with a
 // 128-byte swizzle (one 128-byte row per box row).
@@ -188,6 +207,7 @@ fa::AttnShape make_shape(int B, int H, int N, int d, float scale, int causal) {
   s.N = N;
   s.D = d;
   s.Nk = N;
+  s.Hk = H;
   s.causal = causal ? 1 : 0;
   s.scale = scale;
   s.scale_log2 = scale * fa::kLog2e;
@@ -257,6 +277,8 @@ int apply_test_hooks(cudaStream_t stream) {
   if (e == cudaSuccess) e = fa::set_bwd_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_fp8_test_hooks(limit, drop, stream);
+  if (e == cudaSuccess) e = fa::set_fwd_gqa_test_hooks(limit, drop, stream);
+  if (e == cudaSuccess) e = fa::set_bwd_gqa_test_hooks(limit, drop, stream);
   if (e != cudaSuccess) return launch_error(e);
   applied_limit = limit;
   applied_drop = drop;
@@ -313,13 +335,14 @@ const char* fa_last_cuda_error(void) { return g_last_cuda_error; }
 int fa_check_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return launch_error(e);
-  const int a = fa::take_fwd_status();
-  const int b = fa::take_bwd_status();
-  const int c = fa::take_decode_status();
-  const int f = fa::take_fp8_status();
-  if (a == FA_ERR_LAUNCH || b == FA_ERR_LAUNCH || c == FA_ERR_LAUNCH || f == FA_ERR_LAUNCH)
-    return launch_error(cudaGetLastError());
-  if (a != 0 || b != 0 || c != 0 || f != 0) return FA_ERR_TIMEOUT;
+  const int words[] = {fa::take_fwd_status(), fa::take_bwd_status(),     fa::take_decode_status(),
+                       fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status()};
+  bool late = false;
+  for (int w : words) {
+    if (w == FA_ERR_LAUNCH) return launch_error(cudaGetLastError());
+    late = late || w != 0;
+  }
+  if (late) return FA_ERR_TIMEOUT;
   return FA_OK;
 }
 
@@ -385,6 +408,54 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   fa::LaunchMarks marks;
   const bool timed = next_marks(&marks, 0, 1);
   cudaError_t e = fa::launch_fwd(tq, tk, tv, a, s, timed ? &marks : nullptr);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+// Argument checks that the grouped-head packed entry points share.
+static int check_gqa(int batch, int H, int H_kv, int d, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k,
+                     float scale) {
+  if (total_q < 1 || total_k < 1 || max_seqlen_q < 1 || max_seqlen_k < 1) return FA_ERR_INVALID;
+  if (max_seqlen_q > total_q || max_seqlen_k > total_k) return FA_ERR_INVALID;
+  if (H_kv < 1 || H < 1 || H % H_kv != 0) return FA_ERR_INVALID;
+  const int st = check_shape(batch, H, max_seqlen_q, d, scale);
+  if (st != FA_OK) return st;
+  if (static_cast<long long>(total_q) * H * d > (1LL << 40) || static_cast<long long>(total_k) * H_kv * d > (1LL << 40))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int fa_fwd_varlen_gqa(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_seqlens_q,
+                      const int* cu_seqlens_k, int batch, int H, int H_kv, int d, int total_q, int total_k,
+                      int max_seqlen_q, int max_seqlen_k, float scale, int causal, void* stream) {
+  if (!q || !k || !v || !o || !lse || !cu_seqlens_q || !cu_seqlens_k) return FA_ERR_INVALID;
+  int st = check_gqa(batch, H, H_kv, d, total_q, total_k, max_seqlen_q, max_seqlen_k, scale);
+  if (st != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
+    return FA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s);
+  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s);
+  if (st != FA_OK) return st;
+  st = apply_test_hooks(s);
+  if (st != FA_OK) return st;
+  fa::FwdArgs a;
+  a.qt = q_tile(H / H_kv);
+  CUtensorMap tq, tk, tv;
+  if (!encode_thd_group(&tq, q, H, total_q, d, a.qt) || !encode_thd(&tk, k, H_kv, total_k, d, 128) ||
+      !encode_thd(&tv, v, H_kv, total_k, d, 128))
+    return launch_error(cudaErrorInvalidValue);
+  a.s = make_shape(batch, H, max_seqlen_q, d, scale, causal);
+  a.s.Nk = max_seqlen_k;
+  a.s.Hk = H_kv;
+  a.pk = fa::Packing{1, cu_seqlens_q, cu_seqlens_k, total_q, total_k};
+  a.kv_lens = nullptr;
+  a.o = o;
+  a.lse = lse;
+  fa::LaunchMarks marks;
+  const bool timed = next_marks(&marks, 0, 1);
+  cudaError_t e = fa::launch_fwd_gqa(tq, tk, tv, a, s, timed ? &marks : nullptr);
   if (e != cudaSuccess) return launch_error(e);
   if (check_mode()) return fa_check_status(stream);
   return FA_OK;
@@ -596,6 +667,71 @@ int fa_bwd_varlen_deterministic(const void* q, const void* k, const void* v, con
                                 size_t workspace_bytes, void* stream) {
   return bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, batch, H, d, total_q, total_k,
                     max_seqlen_q, max_seqlen_k, scale, causal, workspace, workspace_bytes, stream, 1);
+}
+
+static int bwd_varlen_gqa(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                          const void* dO, void* dq, void* dk, void* dv, const int* cu_seqlens_q,
+                          const int* cu_seqlens_k, int batch, int H, int H_kv, int d, int total_q, int total_k,
+                          int max_seqlen_q, int max_seqlen_k, float scale, int causal, void* workspace,
+                          size_t workspace_bytes, void* stream, int det) {
+  if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv || !cu_seqlens_q || !cu_seqlens_k)
+    return FA_ERR_INVALID;
+  int st = check_gqa(batch, H, H_kv, d, total_q, total_k, max_seqlen_q, max_seqlen_k, scale);
+  if (st != FA_OK) return st;
+  const void* ptrs[] = {q, k, v, o, lse, dO, dq, dk, dv};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa_bwd_workspace_size(batch, H, max_seqlen_q, d);
+  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s);
+  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s);
+  if (st != FA_OK) return st;
+  st = apply_test_hooks(s);
+  if (st != FA_OK) return st;
+  CUtensorMap tq, tk, tv, tdo;
+  if (!encode_thd(&tq, q, H, total_q, d, 128) || !encode_thd(&tk, k, H_kv, total_k, d, 128) ||
+      !encode_thd(&tv, v, H_kv, total_k, d, 128) || !encode_thd(&tdo, dO, H, total_q, d, 128))
+    return launch_error(cudaErrorInvalidValue);
+  const size_t rows = static_cast<size_t>(batch) * H * ((static_cast<size_t>(max_seqlen_q) + 127) / 128 * 128);
+  fa::BwdArgs a;
+  a.s = make_shape(batch, H, max_seqlen_q, d, scale, causal);
+  a.s.Nk = max_seqlen_k;
+  a.s.Hk = H_kv;
+  a.pk = fa::Packing{1, cu_seqlens_q, cu_seqlens_k, total_q, total_k};
+  a.kv_lens = nullptr;
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  a.dO = dO;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  carve_workspace(&a, workspace, rows, d);
+  a.deterministic = det;
+  fa::LaunchMarks marks;
+  const bool timed = next_marks(&marks, 1, 3);
+  cudaError_t e = fa::launch_bwd_gqa(tq, tk, tv, tdo, a, s, timed ? &marks : nullptr);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+int fa_bwd_varlen_gqa(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                      void* dq, void* dk, void* dv, const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
+                      int H, int H_kv, int d, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k,
+                      float scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  return bwd_varlen_gqa(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, batch, H, H_kv, d, total_q,
+                        total_k, max_seqlen_q, max_seqlen_k, scale, causal, workspace, workspace_bytes, stream, 0);
+}
+
+int fa_bwd_varlen_gqa_deterministic(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                    const void* dO, void* dq, void* dk, void* dv, const int* cu_seqlens_q,
+                                    const int* cu_seqlens_k, int batch, int H, int H_kv, int d, int total_q,
+                                    int total_k, int max_seqlen_q, int max_seqlen_k, float scale, int causal,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  return bwd_varlen_gqa(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, batch, H, H_kv, d, total_q,
+                        total_k, max_seqlen_q, max_seqlen_k, scale, causal, workspace, workspace_bytes, stream, 1);
 }
 
 size_t fa_decode_workspace_size(int B, int H, int d, int max_seq_len) {

@@ -15,6 +15,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct AttnShape {
   int B, H, N, D;    // N: (longest) query sequence length
   int Nk;            // (longest) key sequence length; = N for the fixed layout
+  int Hk;            // key/value heads; = H except in the grouped layouts
   int causal;
   float scale;       // softmax scale applied to Q K^T
   float scale_log2;  // scale * log2(e): logits in base-2 units
@@ -25,6 +26,13 @@ struct AttnShape {
 // Packed layout (varlen = 1): [total, H, d] with sequence b at rows
 // cu_q[b]..cu_q[b+1] (queries) and cu_k[b]..cu_k[b+1] (keys), N = the longest
 // query sequence, causal bottom-right (query i sees key c iff c <= i + Lk - Lq).
+//
+// Grouped layout (LAYOUT kGrouped): the packed layout with Hk key/value heads,
+// query head h reading key head h / G, G = H / Hk. The forward packs several
+// heads of a group into one 128-row Q tile (row = token * P + head), see
+// QTile.
+constexpr int kFixed = 0, kPacked = 1, kGrouped = 2;
+
 struct Packing {
   int varlen;
   const int* cu_q;  // device int32 [B+1]
@@ -37,12 +45,20 @@ struct SeqView {
   int q_start, k_start, Lq, Lk, shift;
 };
 
-// The kernels are compiled once per layout (VARLEN), so the fixed layout
-// carries no packed-layout arithmetic.
-template <bool VARLEN>
-__device__ __forceinline__ SeqView seq_view(const Packing& pk, const int* kv_lens, int b, int N) {
+// The kernels are compiled once per layout, so the fixed layout carries no
+// packed-layout arithmetic. The grouped layout clamps what it reads to the
+// tensors (rows [0, total)) and to the longest lengths the call names (N, Nk),
+// so that offsets that break the contract cannot reach other memory.
+template <int LAYOUT>
+__device__ __forceinline__ SeqView seq_view(const Packing& pk, const int* kv_lens, int b, int N, int Nk) {
   SeqView v;
-  if constexpr (VARLEN) {
+  if constexpr (LAYOUT == kGrouped) {
+    v.q_start = min(max(pk.cu_q[b], 0), pk.total_q);
+    v.Lq = min(max(pk.cu_q[b + 1] - v.q_start, 0), min(N, pk.total_q - v.q_start));
+    v.k_start = min(max(pk.cu_k[b], 0), pk.total_k);
+    v.Lk = min(max(pk.cu_k[b + 1] - v.k_start, 0), min(Nk, pk.total_k - v.k_start));
+    v.shift = v.Lk - v.Lq;
+  } else if constexpr (LAYOUT == kPacked) {
     v.q_start = pk.cu_q[b];
     v.Lq = pk.cu_q[b + 1] - v.q_start;
     v.k_start = pk.cu_k[b];
@@ -60,23 +76,33 @@ __device__ __forceinline__ SeqView seq_view(const Packing& pk, const int* kv_len
 }
 
 // Row index (in units of D elements) of row n of sequence view v, head h
-// (flattened head bh = b * H + h) in a user tensor, and of its LSE entry.
-template <bool VARLEN>
+// (flattened head bh = b * H + h, key heads b * Hk + h) in a user tensor, and
+// of its LSE entry.
+template <int LAYOUT>
 __device__ __forceinline__ size_t q_row(const Packing& pk, const AttnShape& s, const SeqView& v, int bh, int n) {
-  return VARLEN ? (static_cast<size_t>(v.q_start) + n) * s.H + (bh % s.H) : static_cast<size_t>(bh) * s.N + n;
+  return LAYOUT != kFixed ? (static_cast<size_t>(v.q_start) + n) * s.H + (bh % s.H) : static_cast<size_t>(bh) * s.N + n;
 }
-template <bool VARLEN>
+template <int LAYOUT>
 __device__ __forceinline__ size_t k_row(const Packing& pk, const AttnShape& s, const SeqView& v, int bh, int n) {
-  return VARLEN ? (static_cast<size_t>(v.k_start) + n) * s.H + (bh % s.H) : static_cast<size_t>(bh) * s.N + n;
+  const int Hk = LAYOUT == kGrouped ? s.Hk : s.H;
+  return LAYOUT != kFixed ? (static_cast<size_t>(v.k_start) + n) * Hk + (bh % Hk) : static_cast<size_t>(bh) * s.N + n;
 }
-template <bool VARLEN>
+template <int LAYOUT>
 __device__ __forceinline__ size_t lse_index(const Packing& pk, const AttnShape& s, const SeqView& v, int bh, int n) {
-  return VARLEN ? static_cast<size_t>(bh % s.H) * pk.total_q + v.q_start + n : static_cast<size_t>(bh) * s.N + n;
+  return LAYOUT != kFixed ? static_cast<size_t>(bh % s.H) * pk.total_q + v.q_start + n : static_cast<size_t>(bh) * s.N + n;
 }
+
+// How the grouped forward fills a 128-row Q tile: tok tokens x P heads of one
+// key head's group (row = token * P + head; P divides G, tok = 128 / P). Rows
+// past tok * P (P not a power of two) hold nothing and are not written.
+struct QTile {
+  int P, tok;
+};
 
 struct FwdArgs {
   AttnShape s;
   Packing pk;
+  QTile qt;              // grouped layout only
   const int* kv_lens;    // device [B] or nullptr (fixed layout only)
   void* o;               // bf16 [B,H,N,D]
   float* lse;            // fp32 [B,H,N], natural log
@@ -196,6 +222,11 @@ cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
                        cudaStream_t stream, const LaunchMarks* marks);
 cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream, const LaunchMarks* marks);
+// The same for the grouped layout (fwd_gqa.cu, bwd_gqa.cu).
+cudaError_t launch_fwd_gqa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdArgs& a,
+                           cudaStream_t stream, const LaunchMarks* marks);
+cudaError_t launch_bwd_gqa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream, const LaunchMarks* marks);
 // Fixed device scratch of the allocation-free backward (defined in bwd.cu):
 // its device address for the current device (looked up once per device) and
 // its size in bytes.
@@ -210,6 +241,10 @@ cudaError_t set_bwd_test_hooks(unsigned long long wait_limit_ns, int drop_loads,
 // Read and clear the device status word of each kernel translation unit.
 int take_fwd_status();
 int take_bwd_status();
+cudaError_t set_fwd_gqa_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
+cudaError_t set_bwd_gqa_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
+int take_fwd_gqa_status();
+int take_bwd_gqa_status();
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, cudaStream_t stream,
                           const LaunchMarks* marks);
 cudaError_t set_decode_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);

@@ -183,6 +183,35 @@ int fa_bwd_varlen_deterministic(const void* q, const void* k, const void* v, con
                                 size_t workspace_bytes, void* stream);
 
 /*
+ * Prompt attention with grouped heads: fa_fwd_varlen and fa_bwd_varlen with
+ * H_kv <= H key/value heads (H a multiple of H_kv). Query head h reads key
+ * head h / (H / H_kv); everything else (packing, bottom-right causal mask,
+ * empty rows and sequences, scale, LSE) is as there, and H_kv = H computes the
+ * same function. dK and dV are the sums over the query heads of each key head.
+ *   q, o, dO, dq   device bf16 [total_q, H, d];  k, v, dk, dv  [total_k, H_kv, d].
+ *   lse            device fp32 [H, total_q].
+ *   workspace      >= fa_bwd_workspace_size(batch, H, max_seqlen_q, d) bytes.
+ * Rows of no sequence (past cu_seqlens[batch]) are neither read nor written.
+ * Sequences longer than max_seqlen_* or reaching past total_* are cut there
+ * (check mode rejects them). fa_bwd_varlen_gqa_deterministic sums dQ in a
+ * fixed order (bitwise repeatable), like fa_bwd_varlen_deterministic.
+ * Errors: as for the entry points above; FA_ERR_INVALID also when H is not a
+ * multiple of H_kv.
+ */
+int fa_fwd_varlen_gqa(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_seqlens_q,
+                      const int* cu_seqlens_k, int batch, int H, int H_kv, int d, int total_q, int total_k,
+                      int max_seqlen_q, int max_seqlen_k, float scale, int causal, void* stream);
+int fa_bwd_varlen_gqa(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                      void* dq, void* dk, void* dv, const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
+                      int H, int H_kv, int d, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k,
+                      float scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+int fa_bwd_varlen_gqa_deterministic(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                    const void* dO, void* dq, void* dk, void* dv, const int* cu_seqlens_q,
+                                    const int* cu_seqlens_k, int batch, int H, int H_kv, int d, int total_q,
+                                    int total_k, int max_seqlen_q, int max_seqlen_k, float scale, int causal,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * One decoding step over a paged KV cache ("FlashAttention 完整解析", §7.2-7.4:
  * KV cache pages found through a block table). Sequence b has seq_lens[b]
  * cached tokens; token t sits in slot t % block_size of physical block
