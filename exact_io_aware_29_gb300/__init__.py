@@ -36,9 +36,14 @@ from .binding import (  # noqa: F401
     fa_fwd_fp8,
     fa_fwd_varlen,
     fa_fwd_varlen_gqa,
+    fa_qk_norm_rope,
+    fa_qk_norm_rope_bwd,
+    fa_qk_norm_rope_bwd_workspace_size,
     fa_quantize_fp8,
     fa_status_string,
     library_path,
     load_library,
+    qk_norm_rope,
+    qk_norm_rope_backward,
     quantize_fp8,
 )

@@ -28,6 +28,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _P]),
     "fa_fwd_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
@@ -46,6 +47,9 @@ SIGNATURES = {
     "fa_fwd_varlen_gqa": (_I, [_P] * 7 + [_I] * 8 + [_F, _I, _P]),
     "fa_bwd_varlen_gqa": (_I, [_P] * 11 + [_I] * 8 + [_F, _I, _P, ctypes.c_size_t, _P]),
     "fa_bwd_varlen_gqa_deterministic": (_I, [_P] * 11 + [_I] * 8 + [_F, _I, _P, ctypes.c_size_t, _P]),
+    "fa_qk_norm_rope": (_I, [_P] * 9 + [_I] * 6 + [_L, _L, _F, _I, _P]),
+    "fa_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "fa_qk_norm_rope_bwd": (_I, [_P] * 13 + [_I] * 6 + [_L] * 4 + [_F, _I, _P, ctypes.c_size_t, _P]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_last_cuda_error": (ctypes.c_char_p, []),
@@ -468,6 +472,98 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, max_seq_l
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     fa_decode_paged(q, k_cache, v_cache, o, lse, block_table, seq_lens, max_seq_len, scale, workspace, stream)
     return o, lse
+
+
+def _check_heads(name, t, shape=None):
+    """A bf16 [T, H, d] tensor whose heads lie side by side; returns its token stride in elements."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be bfloat16 [T, H, d] with contiguous heads")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions):
+    import torch
+    strides = _check_heads("q", q), _check_heads("k", k)
+    (T, H, d), H_kv = q.shape, k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and head dim")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w.dtype != torch.bfloat16 or tuple(w.shape) != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bfloat16 [d]")
+    if cos.dtype != torch.float32 or cos.dim() != 2 or sin.dtype != torch.float32 or sin.shape != cos.shape \
+            or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous float32 [max_pos, rot / 2]")
+    if positions.dtype != torch.int32 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32 [T]")
+    dev = _on_device(where, q, k, q_weight, k_weight, cos, sin, positions)
+    return dev, strides, (T, H, H_kv, d, 2 * cos.shape[1], cos.shape[0])
+
+
+def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps: float = 1e-6,
+                    interleaved: bool = False, stream=None) -> None:
+    """Per-head norm of q and k with the rotation; same semantics as the C
+    entry point. q and k may be strided over tokens (parts of a fused
+    projection); the rotated width is 2 * cos.shape[1]."""
+    dev, strides, sizes = _check_norm_rope("fa_qk_norm_rope", q, k, q_weight, k_weight, cos, sin, positions)
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        _check_thd(name, t)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    _on_device("fa_qk_norm_rope", q, q_out, k_out)
+    _call("fa_qk_norm_rope", dev, stream, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+          _ptr(positions), _ptr(q_out), _ptr(k_out), *sizes, *strides, float(eps), int(bool(interleaved)))
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps: float = 1e-6, interleaved: bool = False,
+                 stream=None):
+    """Allocates the outputs [T, H, d] and [T, H_kv, d], then calls fa_qk_norm_rope."""
+    import torch
+    q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, stream)
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_bwd_workspace_size(T: int, H: int, H_kv: int, d: int) -> int:
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d))
+
+
+def fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                        eps: float = 1e-6, interleaved: bool = False, workspace=None, stream=None) -> None:
+    """Backward of fa_qk_norm_rope; same semantics as the C entry point. dq
+    and dk may be strided over tokens, like q and k."""
+    import torch
+    where = "fa_qk_norm_rope_bwd"
+    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions)
+    for name, t, like in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        _check_thd(name, t)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    out_strides = _check_heads("dq", dq, q.shape), _check_heads("dk", dk, k.shape)
+    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if w.dtype != torch.float32 or tuple(w.shape) != (q.shape[2],) or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 [d]")
+    if workspace is None:
+        need = fa_qk_norm_rope_bwd_workspace_size(*sizes[:4])
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _on_device(where, q, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace)
+    _call(where, dev, stream, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+          _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), *sizes,
+          *strides, *out_strides, float(eps), int(bool(interleaved)), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+
+
+def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
+                          interleaved: bool = False, workspace=None, stream=None):
+    """Allocates the gradients, then calls fa_qk_norm_rope_bwd. Returns (dq, dk, dq_weight, dk_weight)."""
+    import torch
+    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    dwq, dwk = (torch.empty(q.shape[2], dtype=torch.float32, device=q.device) for _ in range(2))
+    fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dwq, dwk, eps,
+                        interleaved, workspace, stream)
+    return dq, dk, dwq, dwk
 
 
 def fa_quantize_fp8(x, out, block_scale, transpose: bool, stream=None) -> None:

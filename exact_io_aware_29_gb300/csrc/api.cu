@@ -858,4 +858,118 @@ int fa_fwd_fp8(const void* q8, const void* k8, const void* v8t, const float* q_s
   return FA_OK;
 }
 
+// Argument checks and arguments that both directions of the norm + rotation share.
+static int norm_rope_args(fa::NormRopeArgs* a, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const float* cos, const float* sin, const int* positions, int T, int H,
+                          int H_kv, int d, int rot, int max_pos, long long q_stride, long long k_stride, float eps,
+                          int interleaved) {
+  if (!q || !k || !q_weight || !k_weight || !cos || !sin || !positions) return FA_ERR_INVALID;
+  if (H_kv < 1 || max_pos < 1 || rot < 0 || rot > d) return FA_ERR_INVALID;
+  if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID;
+  int st = check_shape(T, H, 1, d, 1.f);
+  if (st == FA_OK) st = check_shape(T, H_kv, 1, d, 1.f);
+  if (st != FA_OK) return st;
+  if (q_stride < static_cast<long long>(H) * d || k_stride < static_cast<long long>(H_kv) * d) return FA_ERR_INVALID;
+  if (rot % 16 != 0 || q_stride % 8 != 0 || k_stride % 8 != 0) return FA_ERR_UNSUPPORTED;
+  if (q_stride > (1LL << 40) / T || k_stride > (1LL << 40) / T) return FA_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k, q_weight, k_weight, cos, sin};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  *a = fa::NormRopeArgs{};
+  a->q = q;
+  a->k = k;
+  a->wq = q_weight;
+  a->wk = k_weight;
+  a->cos = cos;
+  a->sin = sin;
+  a->positions = positions;
+  a->T = T;
+  a->H = H;
+  a->Hk = H_kv;
+  a->D = d;
+  a->rot = rot;
+  a->max_pos = max_pos;
+  a->q_stride = q_stride;
+  a->k_stride = k_stride;
+  a->eps = eps;
+  a->interleaved = interleaved ? 1 : 0;
+  return FA_OK;
+}
+
+// Check mode: copy the positions to the host and validate them.
+static int check_positions(const int* positions, int T, int max_pos, cudaStream_t stream) {
+  if (!check_mode()) return FA_OK;
+  std::vector<int> h(T);
+  cudaError_t e = cudaMemcpyAsync(h.data(), positions, sizeof(int) * T, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return launch_error(e);
+  for (int p : h)
+    if (p < 0 || p >= max_pos) return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+int fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
+                    const float* sin, const int* positions, void* q_out, void* k_out, int T, int H, int H_kv, int d,
+                    int rot, int max_pos, long long q_stride, long long k_stride, float eps, int interleaved,
+                    void* stream) {
+  fa::NormRopeArgs a;
+  if (!q_out || !k_out) return FA_ERR_INVALID;
+  int st = norm_rope_args(&a, q, k, q_weight, k_weight, cos, sin, positions, T, H, H_kv, d, rot, max_pos, q_stride,
+                          k_stride, eps, interleaved);
+  if (st != FA_OK) return st;
+  if (!aligned16(q_out) || !aligned16(k_out)) return FA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_positions(positions, T, max_pos, s);
+  if (st != FA_OK) return st;
+  a.yq = q_out;
+  a.yk = k_out;
+  cudaError_t e = fa::launch_norm_rope(a, s);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int H_kv, int d) {
+  if (check_shape(T, H, 1, d, 1.f) != FA_OK || check_shape(T, H_kv, 1, d, 1.f) != FA_OK) return 0;
+  return static_cast<size_t>(fa::kNormRopeMaxCtas) * 2 * d * sizeof(float);
+}
+
+int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
+                        const float* sin, const int* positions, const void* dq_out, const void* dk_out, void* dq,
+                        void* dk, float* dq_weight, float* dk_weight, int T, int H, int H_kv, int d, int rot,
+                        int max_pos, long long q_stride, long long k_stride, long long dq_stride,
+                        long long dk_stride, float eps, int interleaved, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  fa::NormRopeArgs a;
+  if (!dq_out || !dk_out || !dq || !dk || !dq_weight || !dk_weight) return FA_ERR_INVALID;
+  int st = norm_rope_args(&a, q, k, q_weight, k_weight, cos, sin, positions, T, H, H_kv, d, rot, max_pos, q_stride,
+                          k_stride, eps, interleaved);
+  if (st != FA_OK) return st;
+  if (dq_stride < static_cast<long long>(H) * d || dk_stride < static_cast<long long>(H_kv) * d) return FA_ERR_INVALID;
+  if (dq_stride % 8 != 0 || dk_stride % 8 != 0) return FA_ERR_UNSUPPORTED;
+  if (dq_stride > (1LL << 40) / T || dk_stride > (1LL << 40) / T) return FA_ERR_UNSUPPORTED;
+  const void* ptrs[] = {dq_out, dk_out, dq, dk};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d))
+    return FA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_positions(positions, T, max_pos, s);
+  if (st != FA_OK) return st;
+  a.gq = dq_out;
+  a.gk = dk_out;
+  a.yq = dq;
+  a.yk = dk;
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.part = static_cast<float*>(workspace);
+  cudaError_t e = fa::launch_norm_rope_bwd(a, s);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
 }  // extern "C"

@@ -167,6 +167,25 @@ struct DecodeArgs {
   float* part_ml;           // workspace fp32 [B*H, nsplit, 2]: running max (base 2), sum
 };
 
+// Per-head norm of q and k with the rotation (norm_rope.cu), both directions.
+struct NormRopeArgs {
+  const void *q, *k;          // bf16 rows of d elements, heads side by side, tokens q_stride / k_stride elements apart
+  const void *wq, *wk;        // bf16 [d]
+  const float *cos, *sin;     // fp32 [max_pos, rot / 2]
+  const int* positions;       // int32 [T], clamped to [0, max_pos)
+  const void *gq, *gk;        // backward: bf16 gradients of the outputs, [T, H, d] and [T, Hk, d]
+  void *yq, *yk;              // forward: bf16 [T, H, d] and [T, Hk, d]; backward: gradients of q and k
+  float *dwq, *dwk;           // backward: fp32 [d]
+  float* part;                // backward workspace: fp32 [CTAs][2 d]
+  long long T, q_stride, k_stride, dq_stride, dk_stride;
+  int H, Hk, D, rot, max_pos, interleaved;
+  int rows, q_slices, k_slices;  // set at launch: heads per unit of work, units per token
+  float eps;
+};
+constexpr int kNormRopeMaxCtas = 152 * 4;  // of the backward: one row of partial weight gradients each
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, cudaStream_t stream);
+
 // Key limit of batch b: keys c >= limit are masked (clamped to [0, N]).
 __device__ __forceinline__ int key_limit(const int* kv_lens, int b, int N) {
   if (kv_lens == nullptr) return N;

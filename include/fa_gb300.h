@@ -274,6 +274,50 @@ int fa_fwd_fp8(const void* q8, const void* k8, const void* v8t, const float* q_s
                const float* v_scale, void* o, float* lse, int B, int H, int N, int d, float scale, int causal,
                const int* kv_lens, void* stream);
 
+/*
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass: for every row x (one head of one token, d elements) of q and k,
+ *   u = x * rsqrt(mean(x^2) + eps) * weight,
+ *   out = u, each pair (a, b) of its first `rot` elements replaced by
+ *         (a cos - b sin, b cos + a sin),
+ * with cos and sin taken from row positions[token] of the tables, entry i for
+ * the pair (i, i + rot/2), or (2i, 2i + 1) when `interleaved`. Computed in
+ * fp32 and rounded to bf16 once.
+ *   q, k           device bf16: element e of head h of token t at
+ *                  [t * stride + h * d + e] (strides in elements, multiples of
+ *                  8, >= heads * d), so both can be parts of a fused projection.
+ *   q_weight, k_weight  device bf16 [d].
+ *   cos, sin       device fp32 [max_pos, rot / 2], 16-byte aligned.
+ *   positions      device int32 [T], in [0, max_pos) (check mode rejects others
+ *                  on the host; otherwise they are clamped on the device).
+ *   q_out, k_out   device bf16 [T, H, d] and [T, H_kv, d], contiguous.
+ *   rot            a multiple of 16 in [0, d]; d in {64, 128}; eps >= 0.
+ */
+int fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
+                    const float* sin, const int* positions, void* q_out, void* k_out, int T, int H, int H_kv, int d,
+                    int rot, int max_pos, long long q_stride, long long k_stride, float eps, int interleaved,
+                    void* stream);
+
+/*
+ * Its backward: gradients of sum(q_out * dq_out) + sum(k_out * dk_out).
+ *   q, k, ..., positions   the forward's inputs.
+ *   dq_out, dk_out  device bf16 [T, H, d] and [T, H_kv, d], contiguous.
+ *   dq, dk          device bf16, written, laid out like q and k with strides
+ *                   of their own (elements between a token's heads and the
+ *                   next token's are left as they were).
+ *   dq_weight, dk_weight   device fp32 [d], written: sums over all tokens and
+ *                   heads, in a fixed order (bitwise repeatable).
+ *   workspace       >= fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d) bytes,
+ *                   16-byte aligned, caller-owned; contents on entry are ignored.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int T, int H, int H_kv, int d);
+int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight, const float* cos,
+                        const float* sin, const int* positions, const void* dq_out, const void* dk_out, void* dq,
+                        void* dk, float* dq_weight, float* dk_weight, int T, int H, int H_kv, int d, int rot,
+                        int max_pos, long long q_stride, long long k_stride, long long dq_stride,
+                        long long dk_stride, float eps, int interleaved, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Synchronise `stream`, then read and clear the kernels' device status word:
  * FA_OK, FA_ERR_TIMEOUT, or FA_ERR_LAUNCH for a CUDA error. */
 int fa_check_status(void* stream);

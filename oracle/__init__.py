@@ -23,3 +23,4 @@ from .attention import (  # noqa: F401
     varlen_forward,
     visible,
 )
+from .norm_rope import norm_rope_backward, norm_rope_forward  # noqa: F401
