@@ -18,6 +18,7 @@ from .binding import (  # noqa: F401
     attention_backward_varlen,
     attention_backward_varlen_gqa,
     attention_decode_paged,
+    attention_decode_shared_prefix,
     attention_forward,
     attention_forward_fp8,
     attention_forward_varlen,
@@ -31,6 +32,8 @@ from .binding import (  # noqa: F401
     fa_bwd_workspace_size,
     fa_check_status,
     fa_decode_paged,
+    fa_decode_shared_prefix,
+    fa_decode_shared_prefix_workspace_size,
     fa_decode_workspace_size,
     fa_fwd,
     fa_fwd_fp8,

@@ -50,6 +50,8 @@ SIGNATURES = {
     "fa_qk_norm_rope": (_I, [_P] * 9 + [_I] * 6 + [_L, _L, _F, _I, _P]),
     "fa_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "fa_qk_norm_rope_bwd": (_I, [_P] * 13 + [_I] * 6 + [_L] * 4 + [_F, _I, _P, ctypes.c_size_t, _P]),
+    "fa_decode_shared_prefix_workspace_size": (ctypes.c_size_t, [_I] * 8),
+    "fa_decode_shared_prefix": (_I, [_P] * 10 + [_I] * 12 + [_F, _P, ctypes.c_size_t, _P]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_last_cuda_error": (ctypes.c_char_p, []),
@@ -471,6 +473,64 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, max_seq_l
     o = torch.empty_like(q)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     fa_decode_paged(q, k_cache, v_cache, o, lse, block_table, seq_lens, max_seq_len, scale, workspace, stream)
+    return o, lse
+
+
+def fa_decode_shared_prefix_workspace_size(n_prefix: int, B: int, H: int, H_kv: int, d: int, max_group: int,
+                                           max_prefix_len: int, max_seq_len: int) -> int:
+    return int(load_library().fa_decode_shared_prefix_workspace_size(n_prefix, B, H, H_kv, d, max_group,
+                                                                     max_prefix_len, max_seq_len))
+
+
+def fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
+                            seq_lens, max_group: int, max_prefix_len: int, max_seq_len: int, scale: float,
+                            workspace=None, stream=None) -> None:
+    """One decoding step of sequences that share prefixes, over a paged KV
+    cache with grouped heads; same semantics as the C entry point."""
+    import torch
+    where = "fa_decode_shared_prefix"
+    _check_thd("q", q)
+    _check_thd("o", o)
+    B, H, d = q.shape
+    if o.shape != q.shape:
+        raise ValueError("o must match q")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[3] != d or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bf16 [num_blocks, block_size, H_kv, d]")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    num_blocks, block_size, H_kv, _ = k_cache.shape
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, H]")
+    for name, t, n in (("prefix_table", prefix_table, None), ("block_table", block_table, B)):
+        if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name} must be contiguous int32 [rows, blocks per row]")
+    P = prefix_table.shape[0]
+    for name, t, n in (("prefix_lens", prefix_lens, P), ("cu_prefix_seqs", cu_prefix_seqs, P + 1),
+                       ("seq_lens", seq_lens, B)):
+        if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 [{n}]")
+    max_group, max_prefix_len, max_seq_len = int(max_group), int(max_prefix_len), int(max_seq_len)
+    if workspace is None:
+        need = fa_decode_shared_prefix_workspace_size(P, B, H, H_kv, d, max_group, max_prefix_len, max_seq_len)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    dev = _on_device(where, q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
+                     seq_lens, workspace)
+    _call(where, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(prefix_table),
+          _ptr(prefix_lens), _ptr(cu_prefix_seqs), _ptr(block_table), _ptr(seq_lens), P, B, H, H_kv, d, num_blocks,
+          block_size, prefix_table.shape[1], block_table.shape[1], max_group, max_prefix_len, max_seq_len,
+          float(scale), _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def attention_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
+                                   seq_lens, max_group, max_prefix_len, max_seq_len, scale, workspace=None,
+                                   stream=None):
+    """Allocates O and LSE, then calls fa_decode_shared_prefix. Returns (O, LSE)."""
+    import torch
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
+                            seq_lens, max_group, max_prefix_len, max_seq_len, scale, workspace, stream)
     return o, lse
 
 

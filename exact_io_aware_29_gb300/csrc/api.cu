@@ -254,6 +254,47 @@ int check_decode_tables(const int* seq_lens, const int* table, int B, int max_bl
   return FA_OK;
 }
 
+// How the shared-prefix step splits its keys over CTAs, from the shapes alone
+// (the workspace size depends on it). `base` items (rows x key heads) of
+// `tiles` 64-key tiles: as many splits as bring the item count to `target`,
+// each of whole tiles.
+void split_keys(long long base, long long len, long long target, int* chunk, int* splits) {
+  const long long tiles = std::max<long long>((len + 63) / 64, 1);
+  long long ns = std::min(std::max<long long>(target / std::max<long long>(base, 1), 1), tiles);
+  const long long per = (tiles + ns - 1) / ns;
+  *chunk = static_cast<int>(per * 64);
+  *splits = static_cast<int>((tiles + per - 1) / per);
+}
+void shared_plan(fa::SharedArgs* a) {
+  const int G = a->H / a->Hk;
+  a->prefix_blocks = static_cast<int>((static_cast<long long>(a->max_group) * G + 63) / 64);
+  a->seq_blocks = (G + 63) / 64;
+  // Two CTAs per SM run at a time (152 SMs). A prefix is split into one such
+  // wave of equal parts; the sequences' own parts differ in length, so that
+  // several smaller waves balance better.
+  split_keys(static_cast<long long>(a->P) * a->Hk * a->prefix_blocks, a->max_prefix_len, 304, &a->prefix_chunk,
+             &a->prefix_splits);
+  split_keys(static_cast<long long>(a->B) * a->Hk * a->seq_blocks, a->max_seq_len, 1024, &a->seq_chunk,
+             &a->seq_splits);
+}
+
+// Check mode: the tables and lengths of a shared-prefix step on the host.
+int check_shared_tables(const fa::SharedArgs& a, cudaStream_t stream) {
+  if (!check_mode()) return FA_OK;
+  std::vector<int> cu(a.P + 1);
+  cudaError_t e = cudaMemcpyAsync(cu.data(), a.cu_seqs, sizeof(int) * cu.size(), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return launch_error(e);
+  if (cu[0] < 0 || cu[a.P] > a.B) return FA_ERR_INVALID;
+  for (int p = 0; p < a.P; ++p)
+    if (cu[p + 1] < cu[p] || cu[p + 1] - cu[p] > a.max_group) return FA_ERR_INVALID;
+  const int st = check_decode_tables(a.prefix_lens, a.prefix_table, a.P, a.max_prefix_blocks, a.block_size,
+                                     a.num_blocks, a.max_prefix_len, stream);
+  if (st != FA_OK) return st;
+  return check_decode_tables(a.seq_lens, a.block_table, a.B, a.max_blocks, a.block_size, a.num_blocks, a.max_seq_len,
+                             stream);
+}
+
 // Test hooks, read from the environment on every call: FA_TEST_WAIT_LIMIT_NS
 // bounds each device wait (default 2 s), FA_TEST_DROP_LOADS=1 makes the TMA
 // producers issue no loads so that the dependent waits run out. Used by the
@@ -279,6 +320,7 @@ int apply_test_hooks(cudaStream_t stream) {
   if (e == cudaSuccess) e = fa::set_fp8_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_fwd_gqa_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_bwd_gqa_test_hooks(limit, drop, stream);
+  if (e == cudaSuccess) e = fa::set_decode_shared_test_hooks(limit, drop, stream);
   if (e != cudaSuccess) return launch_error(e);
   applied_limit = limit;
   applied_drop = drop;
@@ -336,7 +378,8 @@ int fa_check_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return launch_error(e);
   const int words[] = {fa::take_fwd_status(), fa::take_bwd_status(),     fa::take_decode_status(),
-                       fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status()};
+                       fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status(),
+                       fa::take_decode_shared_status()};
   bool late = false;
   for (int w : words) {
     if (w == FA_ERR_LAUNCH) return launch_error(cudaGetLastError());
@@ -792,6 +835,99 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
   fa::LaunchMarks marks;
   const bool timed = next_marks(&marks, 4, pl.nsplit > 1 ? 2 : 1);
   cudaError_t e = fa::launch_decode(tk, tv, a, s, timed ? &marks : nullptr);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+// Sizes of a shared-prefix step, checked, and its plan.
+static int shared_sizes(fa::SharedArgs* a, int n_prefix, int B, int H, int H_kv, int d, int max_group,
+                        int max_prefix_len, int max_seq_len, float scale) {
+  if (n_prefix < 1 || max_group < 1 || H < 1 || H_kv < 1 || H % H_kv != 0) return FA_ERR_INVALID;
+  if (max_group > B) return FA_ERR_INVALID;
+  int st = check_shape(B, H, max_prefix_len, d, scale);
+  if (st == FA_OK) st = check_shape(B, H, max_seq_len, d, scale);
+  if (st == FA_OK) st = check_shape(n_prefix, H, 1, d, scale);
+  if (st != FA_OK) return st;
+  *a = fa::SharedArgs{};
+  a->P = n_prefix;
+  a->B = B;
+  a->H = H;
+  a->Hk = H_kv;
+  a->D = d;
+  a->max_group = max_group;
+  a->max_prefix_len = max_prefix_len;
+  a->max_seq_len = max_seq_len;
+  a->scale_log2 = scale * fa::kLog2e;
+  shared_plan(a);
+  return FA_OK;
+}
+
+// Bytes of the partial O, then of the partial sums, of a plan.
+static size_t shared_part_bytes(const fa::SharedArgs& a, size_t* o_bytes) {
+  const size_t parts = static_cast<size_t>(a.B) * a.H * (a.prefix_splits + a.seq_splits);
+  *o_bytes = align_up(parts * a.D * 4, 256);
+  return *o_bytes + align_up(parts * 4, 256);
+}
+
+size_t fa_decode_shared_prefix_workspace_size(int n_prefix, int B, int H, int H_kv, int d, int max_group,
+                                              int max_prefix_len, int max_seq_len) {
+  fa::SharedArgs a;
+  if (shared_sizes(&a, n_prefix, B, H, H_kv, d, max_group, max_prefix_len, max_seq_len, 1.f) != FA_OK) return 0;
+  size_t o_bytes;
+  return shared_part_bytes(a, &o_bytes);
+}
+
+int fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                            const int* prefix_table, const int* prefix_lens, const int* cu_prefix_seqs,
+                            const int* block_table, const int* seq_lens, int n_prefix, int B, int H, int H_kv, int d,
+                            int num_blocks, int block_size, int max_prefix_blocks, int max_blocks_per_seq,
+                            int max_group, int max_prefix_len, int max_seq_len, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !o || !lse || !prefix_table || !prefix_lens || !cu_prefix_seqs || !block_table ||
+      !seq_lens)
+    return FA_ERR_INVALID;
+  if (num_blocks < 1 || block_size < 1 || max_prefix_blocks < 1 || max_blocks_per_seq < 1) return FA_ERR_INVALID;
+  fa::SharedArgs a;
+  int st = shared_sizes(&a, n_prefix, B, H, H_kv, d, max_group, max_prefix_len, max_seq_len, scale);
+  if (st != FA_OK) return st;
+  if (block_size % 64 != 0) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_prefix_len) > static_cast<long long>(max_prefix_blocks) * block_size ||
+      static_cast<long long>(max_seq_len) > static_cast<long long>(max_blocks_per_seq) * block_size)
+    return FA_ERR_INVALID;
+  if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k_cache, v_cache, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  size_t o_bytes;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < shared_part_bytes(a, &o_bytes))
+    return FA_ERR_WORKSPACE;
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  a.prefix_table = prefix_table;
+  a.prefix_lens = prefix_lens;
+  a.cu_seqs = cu_prefix_seqs;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_prefix_blocks = max_prefix_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_shared_tables(a, s);
+  if (st != FA_OK) return st;
+  st = apply_test_hooks(s);
+  if (st != FA_OK) return st;
+  CUtensorMap tk, tv;
+  const int rows = num_blocks * block_size;
+  if (!encode_thd(&tk, k_cache, H_kv, rows, d, 64) || !encode_thd(&tv, v_cache, H_kv, rows, d, 64))
+    return launch_error(cudaErrorInvalidValue);
+  fa::LaunchMarks marks;
+  const bool timed = next_marks(&marks, 4, 2);
+  cudaError_t e = fa::launch_decode_shared(tk, tv, a, s, timed ? &marks : nullptr);
   if (e != cudaSuccess) return launch_error(e);
   if (check_mode()) return fa_check_status(stream);
   return FA_OK;

@@ -167,6 +167,37 @@ struct DecodeArgs {
   float* part_ml;           // workspace fp32 [B*H, nsplit, 2]: running max (base 2), sum
 };
 
+// Optional CUDA events recorded around each kernel a launcher issues
+// (index = kernel order within the call); nullptr = no timing.
+struct LaunchMarks {
+  cudaEvent_t start[3];
+  cudaEvent_t stop[3];
+};
+
+// One decoding step of sequences that share prefixes (decode_shared.cu).
+struct SharedArgs {
+  const void* q;            // bf16 [B, H, D]
+  void* o;                  // bf16 [B, H, D]
+  float* lse;               // fp32 [B, H], natural log
+  const int* prefix_table;  // int32 [P, max_prefix_blocks]
+  const int* prefix_lens;   // int32 [P], clamped to [0, max_prefix_len]
+  const int* cu_seqs;       // int32 [P + 1]: sequences of each prefix, at most max_group
+  const int* block_table;   // int32 [B, max_blocks]
+  const int* seq_lens;      // int32 [B], clamped to [0, max_seq_len]
+  int P, B, H, Hk, D;
+  int block_size, num_blocks, max_prefix_blocks, max_blocks, max_group, max_prefix_len, max_seq_len;
+  // The plan (api.cu): key ranges of `chunk` keys, `splits` of them per row,
+  // and row blocks of 64, of the prefix part and of the sequences' own part.
+  int prefix_chunk, prefix_splits, prefix_blocks, seq_chunk, seq_splits, seq_blocks;
+  float scale_log2;         // scale * log2(e)
+  float* part_o;            // workspace fp32 [B*H, prefix_splits + seq_splits, D], normalised
+  float* part_lse;          // workspace fp32 [B*H, prefix_splits + seq_splits], base 2
+};
+cudaError_t launch_decode_shared(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
+                                 cudaStream_t stream, const LaunchMarks* marks);
+cudaError_t set_decode_shared_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
+int take_decode_shared_status();
+
 // Per-head norm of q and k with the rotation (norm_rope.cu), both directions.
 struct NormRopeArgs {
   const void *q, *k;          // bf16 rows of d elements, heads side by side, tokens q_stride / k_stride elements apart
@@ -192,13 +223,6 @@ __device__ __forceinline__ int key_limit(const int* kv_lens, int b, int N) {
   int L = kv_lens[b];
   return L < 0 ? 0 : (L > N ? N : L);
 }
-
-// Optional CUDA events recorded around each kernel a launcher issues
-// (index = kernel order within the call); nullptr = no timing.
-struct LaunchMarks {
-  cudaEvent_t start[3];
-  cudaEvent_t stop[3];
-};
 
 inline void mark(const LaunchMarks* m, bool start, int i, cudaStream_t s) {
   if (m != nullptr) cudaEventRecord(start ? m->start[i] : m->stop[i], s);

@@ -242,6 +242,50 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
                     size_t workspace_bytes, void* stream);
 
 /*
+ * One decoding step over a paged KV cache for a batch whose sequences share
+ * long prefixes, with grouped heads: the attention to a prefix is computed
+ * once for all sequences behind it instead of once per sequence. The cache
+ * and its pages are those of fa_decode_paged with H_kv key/value heads (query
+ * head h reads key head h / (H / H_kv)).
+ * Sequences cu_prefix_seqs[p] .. cu_prefix_seqs[p+1]-1 share prefix p, whose
+ * prefix_lens[p] tokens lie in the blocks of prefix_table row p; sequence b's
+ * own seq_lens[b] tokens follow them in the blocks of block_table row b,
+ * starting at slot 0 of the first. The new query of each (sequence, head)
+ * attends to all of both (its own K/V is expected to be in the cache already):
+ *   O[b,h] = softmax(scale * q[b,h] . [K_prefix; K_own]^T) [V_prefix; V_own].
+ * Without sharing (every prefix_lens[p] = 0, or sequences of no prefix) it is
+ * a paged decoding step with grouped heads.
+ *   q, o           device bf16 [B, H, d];  lse  device fp32 [B, H] (natural log;
+ *                  -inf and O = 0 for a sequence with no keys at all).
+ *   k_cache, v_cache  device bf16 [num_blocks, block_size, H_kv, d].
+ *   prefix_table   device int32 [n_prefix, max_prefix_blocks];  prefix_lens
+ *                  device int32 [n_prefix], each in [0, max_prefix_len].
+ *   cu_prefix_seqs device int32 [n_prefix + 1], non-decreasing, in [0, B], at
+ *                  most max_group (<= B) apart. Sequences before the first and
+ *                  from the last entry on have no prefix.
+ *   block_table    device int32 [B, max_blocks_per_seq];  seq_lens device int32
+ *                  [B], each in [0, max_seq_len]. Entries past the last page of
+ *                  a prefix or sequence are not read.
+ *   block_size     a multiple of 64; max_*_len >= 1, at most what the table
+ *                  rows hold.
+ *   workspace      >= fa_decode_shared_prefix_workspace_size(...) bytes,
+ *                  16-byte aligned, caller-owned. Calls that overlap on the
+ *                  GPU need workspaces of their own.
+ * Results are bitwise repeatable. Lengths, offsets and tables are checked on
+ * the host only in check mode (FA_CHECK=1); otherwise lengths and groups are
+ * clamped to the bounds above and block ids outside [0, num_blocks) read as
+ * zero keys and values. Errors as for fa_decode_paged.
+ */
+size_t fa_decode_shared_prefix_workspace_size(int n_prefix, int B, int H, int H_kv, int d, int max_group,
+                                              int max_prefix_len, int max_seq_len);
+int fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                            const int* prefix_table, const int* prefix_lens, const int* cu_prefix_seqs,
+                            const int* block_table, const int* seq_lens, int n_prefix, int B, int H, int H_kv, int d,
+                            int num_blocks, int block_size, int max_prefix_blocks, int max_blocks_per_seq,
+                            int max_group, int max_prefix_len, int max_seq_len, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * FP8 (E4M3) block quantisation ("flash_attention.zh" §9.2: block
  * quantisation, one scale factor per block; "FlashAttention 完整解析" §5.5:
  * E4M3, range +-448). For every 128-row block of every (b, h) slice of the

@@ -24,3 +24,4 @@ from .attention import (  # noqa: F401
     visible,
 )
 from .norm_rope import norm_rope_backward, norm_rope_forward  # noqa: F401
+from .shared import shared_prefix_decode_forward  # noqa: F401
