@@ -233,57 +233,95 @@ def attention_backward_varlen(q, k, v, o, lse, dO, cu_seqlens_q, cu_seqlens_k, m
     return dq, dk, dv
 
 
-def _on_device(where, first, *tensors):
-    """The device of a call whose tensors must all live on it."""
-    dev = first.device
-    if dev.type != "cuda":
+# ---------------------------------------------------------------------------
+# The grouped-head operators are called once per layer and token, where the
+# host's time counts: their checks go over each tensor once.
+# ---------------------------------------------------------------------------
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _want(where, name, t, dtype, shape, dev) -> None:
+    """t must be contiguous, of this dtype and shape, on CUDA device ``dev``."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}; "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+
+
+def _cuda_index(where, t) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise ValueError(f"{where} needs CUDA tensors")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
     return dev
 
 
-def _call(where, dev, stream, *args):
-    """Calls the C entry point ``where`` with ``dev`` current, on ``stream``
-    (None: the current stream of ``dev``) as its last argument."""
-    import torch
+def _alloc(stream, make):
+    """make() with the tensors belonging to the stream that the call runs on:
+    what another stream may still be using is not handed to it, and what it
+    uses is not handed to another one when the tensor dies."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to {dev}")
-    fn = getattr(load_library(), where)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+        return make()
+    with _load_torch().cuda.stream(stream):
+        return make()
+
+
+def _workspace(where, t, need, dev, stream):
+    """The caller's workspace, or one of need() bytes: (tensor, pointer, bytes)."""
+    if t is None:
+        t = _alloc(stream, lambda: _torch.empty(max(need(), 1), dtype=_torch.uint8, device=f"cuda:{dev}"))
+    elif t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: workspace must be a contiguous tensor on cuda:{dev}")
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(where, dev, stream, *args) -> None:
+    """Calls the C entry point ``where`` with device ``dev`` current, on
+    ``stream`` (None: the current stream of ``dev``) as its last argument."""
+    torch = _torch
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    fn = getattr(_LIB or load_library(), where)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, raw)
     if st != FA_OK:
         raise FaError(st, where)
 
 
 def _check_gqa(where, q, k, v, q_like, k_like, lse, cu_seqlens_q, cu_seqlens_k):
     """Shapes of a grouped-head packed call: (device, the C call's sizes up to total_k)."""
-    import torch
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_thd(name, t)
-    (total_q, H, d), (total_k, H_kv, _) = q.shape, k.shape
-    for like, ts in ((q, q_like), (k, (("v", v),) + k_like)):
-        for name, t in ts:
-            _check_thd(name, t)
-            if t.shape != like.shape:
-                raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    if k.shape[2] != d or H_kv < 1 or H % H_kv:
-        raise ValueError("k and v must have q's head dim and a number of heads that divides q's")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [H, total_q] CUDA tensor")
-    _check_cu("cu_seqlens_q", cu_seqlens_q)
+    torch = _load_torch()
+    dev = _cuda_index(where, q)
+    qs, ks, bf16 = q.shape, k.shape, torch.bfloat16
+    if len(qs) != 3 or len(ks) != 3 or ks[2] != qs[2] or ks[1] < 1 or qs[1] % ks[1]:
+        raise ValueError(f"{where}: q is [total_q, H, d], k and v [total_k, H_kv, d] with H a multiple of H_kv; got "
+                         f"{tuple(qs)} and {tuple(ks)}")
+    total_q, H, d = qs
+    _want(where, "q", q, bf16, qs, dev)
+    _want(where, "k", k, bf16, ks, dev)
+    _want(where, "v", v, bf16, ks, dev)
+    for name, t in q_like:
+        _want(where, name, t, bf16, qs, dev)
+    for name, t in k_like:
+        _want(where, name, t, bf16, ks, dev)
+    _want(where, "lse", lse, torch.float32, (H, total_q), dev)
     batch = cu_seqlens_q.numel() - 1
-    _check_cu("cu_seqlens_k", cu_seqlens_k, batch)
-    if not cu_seqlens_q.is_contiguous() or not cu_seqlens_k.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous")
-    dev = _on_device(where, q, k, v, lse, cu_seqlens_q, cu_seqlens_k, *(t for _, t in q_like + k_like))
-    return dev, (batch, H, H_kv, d, total_q, total_k)
+    _want(where, "cu_seqlens_q", cu_seqlens_q, torch.int32, (batch + 1,), dev)
+    _want(where, "cu_seqlens_k", cu_seqlens_k, torch.int32, (batch + 1,), dev)
+    return dev, (batch, H, ks[1], d, total_q, ks[0])
 
 
 def fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
@@ -291,33 +329,30 @@ def fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q:
     """Packed forward with grouped heads (q [total_q, H, d], k and v
     [total_k, H_kv, d]); same semantics as the C entry point."""
     dev, sizes = _check_gqa("fa_fwd_varlen_gqa", q, k, v, (("o", o),), (), lse, cu_seqlens_q, cu_seqlens_k)
-    _call("fa_fwd_varlen_gqa", dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q),
-          _ptr(cu_seqlens_k), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)))
+    _call("fa_fwd_varlen_gqa", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)))
 
 
 def attention_forward_varlen_gqa(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
                                  stream=None):
     """Allocates O [total_q, H, d] and LSE [H, total_q], then calls fa_fwd_varlen_gqa."""
-    import torch
-    o = torch.empty_like(q)
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    torch = _load_torch()
+    o, lse = _alloc(stream, lambda: (torch.empty_like(q), torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32,
+                                                                      device=q.device)))
     fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal, stream)
     return o, lse
 
 
 def _bwd_varlen_gqa(fn, q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                     scale, causal, workspace, stream) -> None:
-    import torch
     dev, sizes = _check_gqa(fn, q, k, v, (("o", o), ("dO", dO), ("dq", dq)), (("dk", dk), ("dv", dv)), lse,
                             cu_seqlens_q, cu_seqlens_k)
-    if workspace is None:
-        need = fa_bwd_workspace_size(sizes[0], sizes[1], int(max_seqlen_q), sizes[3])
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    else:
-        _on_device(fn, q, workspace)
-    _call(fn, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
-          _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale),
-          int(bool(causal)), _ptr(workspace), workspace.numel() * workspace.element_size())
+    workspace, ws, ws_bytes = _workspace(
+        fn, workspace, lambda: fa_bwd_workspace_size(sizes[0], sizes[1], int(max_seqlen_q), sizes[3]), dev,
+        stream)
+    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes,
+          int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)), ws, ws_bytes)
 
 
 def fa_bwd_varlen_gqa(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
@@ -339,8 +374,8 @@ def attention_backward_varlen_gqa(q, k, v, o, lse, dO, cu_seqlens_q, cu_seqlens_
                                   scale, causal, workspace=None, stream=None, deterministic: bool = False):
     """Allocates dQ, dK, dV, then calls fa_bwd_varlen_gqa (or its deterministic
     form). Returns (dQ, dK, dV)."""
-    import torch
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    torch = _load_torch()
+    dq, dk, dv = _alloc(stream, lambda: [torch.empty_like(t) for t in (q, k, v)])
     fn = fa_bwd_varlen_gqa_deterministic if deterministic else fa_bwd_varlen_gqa
     fn(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
        workspace, stream)
@@ -487,79 +522,72 @@ def fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_le
                             workspace=None, stream=None) -> None:
     """One decoding step of sequences that share prefixes, over a paged KV
     cache with grouped heads; same semantics as the C entry point."""
-    import torch
+    torch = _load_torch()
     where = "fa_decode_shared_prefix"
-    _check_thd("q", q)
-    _check_thd("o", o)
-    B, H, d = q.shape
-    if o.shape != q.shape:
-        raise ValueError("o must match q")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[3] != d or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bf16 [num_blocks, block_size, H_kv, d]")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    num_blocks, block_size, H_kv, _ = k_cache.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous float32 [B, H]")
-    for name, t, n in (("prefix_table", prefix_table, None), ("block_table", block_table, B)):
-        if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-            raise ValueError(f"{name} must be contiguous int32 [rows, blocks per row]")
-    P = prefix_table.shape[0]
-    for name, t, n in (("prefix_lens", prefix_lens, P), ("cu_prefix_seqs", cu_prefix_seqs, P + 1),
-                       ("seq_lens", seq_lens, B)):
-        if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous int32 [{n}]")
+    dev = _cuda_index(where, q)
+    qs, cs, bf16, i32 = q.shape, k_cache.shape, torch.bfloat16, torch.int32
+    if len(qs) != 3 or len(cs) != 4 or cs[3] != qs[2] or prefix_table.dim() != 2 or block_table.dim() != 2:
+        raise ValueError(f"{where}: q is [B, H, d], the caches [num_blocks, block_size, H_kv, d], the tables "
+                         f"[rows, blocks per row]; got {tuple(qs)} and {tuple(cs)}")
+    B, H, d = qs
+    P, prefix_width = prefix_table.shape
+    width = block_table.shape[1]
+    _want(where, "q", q, bf16, qs, dev)
+    _want(where, "k_cache", k_cache, bf16, cs, dev)
+    _want(where, "v_cache", v_cache, bf16, cs, dev)
+    _want(where, "o", o, bf16, qs, dev)
+    _want(where, "lse", lse, torch.float32, (B, H), dev)
+    _want(where, "prefix_table", prefix_table, i32, (P, prefix_width), dev)
+    _want(where, "prefix_lens", prefix_lens, i32, (P,), dev)
+    _want(where, "cu_prefix_seqs", cu_prefix_seqs, i32, (P + 1,), dev)
+    _want(where, "block_table", block_table, i32, (B, width), dev)
+    _want(where, "seq_lens", seq_lens, i32, (B,), dev)
     max_group, max_prefix_len, max_seq_len = int(max_group), int(max_prefix_len), int(max_seq_len)
-    if workspace is None:
-        need = fa_decode_shared_prefix_workspace_size(P, B, H, H_kv, d, max_group, max_prefix_len, max_seq_len)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    dev = _on_device(where, q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
-                     seq_lens, workspace)
-    _call(where, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(prefix_table),
-          _ptr(prefix_lens), _ptr(cu_prefix_seqs), _ptr(block_table), _ptr(seq_lens), P, B, H, H_kv, d, num_blocks,
-          block_size, prefix_table.shape[1], block_table.shape[1], max_group, max_prefix_len, max_seq_len,
-          float(scale), _ptr(workspace), workspace.numel() * workspace.element_size())
+    workspace, ws, ws_bytes = _workspace(where, workspace, lambda: fa_decode_shared_prefix_workspace_size(
+        P, B, H, cs[2], d, max_group, max_prefix_len, max_seq_len), dev, stream)
+    _call(where, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          prefix_table.data_ptr(), prefix_lens.data_ptr(), cu_prefix_seqs.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), P, B, H, cs[2], d, cs[0], cs[1], prefix_width, width, max_group, max_prefix_len,
+          max_seq_len, float(scale), ws, ws_bytes)
 
 
 def attention_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
                                    seq_lens, max_group, max_prefix_len, max_seq_len, scale, workspace=None,
                                    stream=None):
     """Allocates O and LSE, then calls fa_decode_shared_prefix. Returns (O, LSE)."""
-    import torch
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    torch = _load_torch()
+    o, lse = _alloc(stream, lambda: (torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)))
     fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
                             seq_lens, max_group, max_prefix_len, max_seq_len, scale, workspace, stream)
     return o, lse
 
 
-def _check_heads(name, t, shape=None):
-    """A bf16 [T, H, d] tensor whose heads lie side by side; returns its token stride in elements."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be bfloat16 [T, H, d] with contiguous heads")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+def _heads_stride(where, name, t, T, H, d, dev) -> int:
+    """The token stride, in elements, of a bf16 [T, H, d] tensor whose heads lie side by side."""
+    st = t.stride()
+    if t.dtype is not _torch.bfloat16 or t.shape != (T, H, d) or st[2] != 1 or (H > 1 and st[1] != d) \
+            or t.get_device() != dev:
+        raise ValueError(f"{where}: {name} must be a bfloat16 tensor of shape {(T, H, d)} with contiguous heads on "
+                         f"cuda:{dev}; got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return st[0] if T > 1 else H * d
 
 
 def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions):
-    import torch
-    strides = _check_heads("q", q), _check_heads("k", k)
-    (T, H, d), H_kv = q.shape, k.shape[1]
-    if k.shape[0] != T or k.shape[2] != d:
-        raise ValueError("q and k must have the same tokens and head dim")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w.dtype != torch.bfloat16 or tuple(w.shape) != (d,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bfloat16 [d]")
-    if cos.dtype != torch.float32 or cos.dim() != 2 or sin.dtype != torch.float32 or sin.shape != cos.shape \
-            or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous float32 [max_pos, rot / 2]")
-    if positions.dtype != torch.int32 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
-        raise ValueError("positions must be contiguous int32 [T]")
-    dev = _on_device(where, q, k, q_weight, k_weight, cos, sin, positions)
-    return dev, strides, (T, H, H_kv, d, 2 * cos.shape[1], cos.shape[0])
+    """(device, token strides of q and k, the C call's sizes)."""
+    torch = _load_torch()
+    dev = _cuda_index(where, q)
+    qs, ks, table = q.shape, k.shape, cos.shape
+    if len(qs) != 3 or len(ks) != 3 or len(table) != 2:
+        raise ValueError(f"{where}: q is [T, H, d], k [T, H_kv, d], cos and sin [max_pos, rot / 2]; got {tuple(qs)}, "
+                         f"{tuple(ks)} and {tuple(table)}")
+    T, H, d = qs
+    strides = _heads_stride(where, "q", q, T, H, d, dev), _heads_stride(where, "k", k, T, ks[1], d, dev)
+    _want(where, "q_weight", q_weight, torch.bfloat16, (d,), dev)
+    _want(where, "k_weight", k_weight, torch.bfloat16, (d,), dev)
+    _want(where, "cos", cos, torch.float32, table, dev)
+    _want(where, "sin", sin, torch.float32, table, dev)
+    _want(where, "positions", positions, torch.int32, (T,), dev)
+    return dev, strides, (T, H, ks[1], d, 2 * table[1], table[0])
 
 
 def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps: float = 1e-6,
@@ -567,21 +595,20 @@ def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out,
     """Per-head norm of q and k with the rotation; same semantics as the C
     entry point. q and k may be strided over tokens (parts of a fused
     projection); the rotated width is 2 * cos.shape[1]."""
-    dev, strides, sizes = _check_norm_rope("fa_qk_norm_rope", q, k, q_weight, k_weight, cos, sin, positions)
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        _check_thd(name, t)
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    _on_device("fa_qk_norm_rope", q, q_out, k_out)
-    _call("fa_qk_norm_rope", dev, stream, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-          _ptr(positions), _ptr(q_out), _ptr(k_out), *sizes, *strides, float(eps), int(bool(interleaved)))
+    where = "fa_qk_norm_rope"
+    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions)
+    _want(where, "q_out", q_out, _torch.bfloat16, q.shape, dev)
+    _want(where, "k_out", k_out, _torch.bfloat16, k.shape, dev)
+    _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
+          sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *sizes, *strides, float(eps),
+          int(bool(interleaved)))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps: float = 1e-6, interleaved: bool = False,
                  stream=None):
     """Allocates the outputs [T, H, d] and [T, H_kv, d], then calls fa_qk_norm_rope."""
-    import torch
-    q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    torch = _load_torch()
+    q_out, k_out = _alloc(stream, lambda: [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)])
     fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved, stream)
     return q_out, k_out
 
@@ -594,33 +621,29 @@ def fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, d
                         eps: float = 1e-6, interleaved: bool = False, workspace=None, stream=None) -> None:
     """Backward of fa_qk_norm_rope; same semantics as the C entry point. dq
     and dk may be strided over tokens, like q and k."""
-    import torch
     where = "fa_qk_norm_rope_bwd"
     dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions)
-    for name, t, like in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        _check_thd(name, t)
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    out_strides = _check_heads("dq", dq, q.shape), _check_heads("dk", dk, k.shape)
-    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if w.dtype != torch.float32 or tuple(w.shape) != (q.shape[2],) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous float32 [d]")
-    if workspace is None:
-        need = fa_qk_norm_rope_bwd_workspace_size(*sizes[:4])
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _on_device(where, q, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace)
-    _call(where, dev, stream, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-          _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), *sizes,
-          *strides, *out_strides, float(eps), int(bool(interleaved)), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+    T, H, H_kv, d = sizes[:4]
+    _want(where, "dq_out", dq_out, _torch.bfloat16, q.shape, dev)
+    _want(where, "dk_out", dk_out, _torch.bfloat16, k.shape, dev)
+    out_strides = _heads_stride(where, "dq", dq, T, H, d, dev), _heads_stride(where, "dk", dk, T, H_kv, d, dev)
+    _want(where, "dq_weight", dq_weight, _torch.float32, (d,), dev)
+    _want(where, "dk_weight", dk_weight, _torch.float32, (d,), dev)
+    workspace, ws, ws_bytes = _workspace(where, workspace,
+                                         lambda: fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d), dev, stream)
+    _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
+          sin.data_ptr(), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+          dq_weight.data_ptr(), dk_weight.data_ptr(), *sizes, *strides, *out_strides, float(eps),
+          int(bool(interleaved)), ws, ws_bytes)
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
                           interleaved: bool = False, workspace=None, stream=None):
     """Allocates the gradients, then calls fa_qk_norm_rope_bwd. Returns (dq, dk, dq_weight, dk_weight)."""
-    import torch
-    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    dwq, dwk = (torch.empty(q.shape[2], dtype=torch.float32, device=q.device) for _ in range(2))
+    torch = _load_torch()
+    dq, dk, dwq, dwk = _alloc(stream, lambda: [
+        *(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)),
+        *(torch.empty(q.shape[2], dtype=torch.float32, device=q.device) for _ in range(2))])
     fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dwq, dwk, eps,
                         interleaved, workspace, stream)
     return dq, dk, dwq, dwk
