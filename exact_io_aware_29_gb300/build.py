@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfa_gb300.so")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "decode.cu", "fp8.cu", "fwd_gqa.cu", "bwd_gqa.cu",
-           "norm_rope.cu", "decode_shared.cu"]
+           "norm_rope.cu", "decode_shared.cu", "decode_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -267,15 +267,35 @@ void split_keys(long long base, long long len, long long target, int* chunk, int
 }
 void shared_plan(fa::SharedArgs* a) {
   const int G = a->H / a->Hk;
-  a->prefix_blocks = static_cast<int>((static_cast<long long>(a->max_group) * G + 63) / 64);
+  const long long group_rows = static_cast<long long>(a->max_group) * G;
   a->seq_blocks = (G + 63) / 64;
   // Two CTAs per SM run at a time (152 SMs). A prefix is split into one such
   // wave of equal parts; the sequences' own parts differ in length, so that
   // several smaller waves balance better.
-  split_keys(static_cast<long long>(a->P) * a->Hk * a->prefix_blocks, a->max_prefix_len, 304, &a->prefix_chunk,
-             &a->prefix_splits);
   split_keys(static_cast<long long>(a->B) * a->Hk * a->seq_blocks, a->max_seq_len, 1024, &a->seq_chunk,
              &a->seq_splits);
+  a->prefix_tiles = group_rows > 32;
+  if (!a->prefix_tiles) {
+    a->prefix_blocks = static_cast<int>((group_rows + 63) / 64);
+    split_keys(static_cast<long long>(a->P) * a->Hk * a->prefix_blocks, a->max_prefix_len, 304, &a->prefix_chunk,
+               &a->prefix_splits);
+    return;
+  }
+  // 128-row tiles, two per CTA and one CTA per SM: the number of splits whose
+  // waves take the least time, a CTA costing its 128-key blocks and about
+  // three more to start and to write its part.
+  const fa::QTile qt = q_tile(G);
+  const long long base = static_cast<long long>(a->P) * (a->H / qt.P) * ((a->max_group + 2 * qt.tok - 1) / (2 * qt.tok));
+  const long long blocks = (static_cast<long long>(a->max_prefix_len) + 127) / 128;
+  long long best = -1;
+  for (long long ns = 1; ns <= std::min<long long>(blocks, 152); ++ns) {
+    const long long per = (blocks + ns - 1) / ns, n = (blocks + per - 1) / per;
+    const long long cost = (base * n + 151) / 152 * (per + 3);
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    a->prefix_chunk = static_cast<int>(per * 128);
+    a->prefix_splits = static_cast<int>(n);
+  }
 }
 
 // Check mode: the tables and lengths of a shared-prefix step on the host.
@@ -321,6 +341,7 @@ int apply_test_hooks(cudaStream_t stream) {
   if (e == cudaSuccess) e = fa::set_fwd_gqa_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_bwd_gqa_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_shared_test_hooks(limit, drop, stream);
+  if (e == cudaSuccess) e = fa::set_decode_prefix_test_hooks(limit, drop, stream);
   if (e != cudaSuccess) return launch_error(e);
   applied_limit = limit;
   applied_drop = drop;
@@ -379,7 +400,7 @@ int fa_check_status(void* stream) {
   if (e != cudaSuccess) return launch_error(e);
   const int words[] = {fa::take_fwd_status(), fa::take_bwd_status(),     fa::take_decode_status(),
                        fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status(),
-                       fa::take_decode_shared_status()};
+                       fa::take_decode_shared_status(), fa::take_decode_prefix_status()};
   bool late = false;
   for (int w : words) {
     if (w == FA_ERR_LAUNCH) return launch_error(cudaGetLastError());
@@ -927,6 +948,13 @@ int fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_ca
     return launch_error(cudaErrorInvalidValue);
   fa::LaunchMarks marks;
   const bool timed = next_marks(&marks, 4, 2);
+  if (a.prefix_tiles) {
+    const fa::QTile qt = q_tile(H / H_kv);
+    CUtensorMap tq;
+    if (!encode_thd_group(&tq, q, H, B, d, qt)) return launch_error(cudaErrorInvalidValue);
+    const cudaError_t pe = fa::launch_decode_prefix(tq, tk, tv, a, qt, s);
+    if (pe != cudaSuccess) return launch_error(pe);
+  }
   cudaError_t e = fa::launch_decode_shared(tk, tv, a, s, timed ? &marks : nullptr);
   if (e != cudaSuccess) return launch_error(e);
   if (check_mode()) return fa_check_status(stream);

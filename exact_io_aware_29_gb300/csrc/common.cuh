@@ -31,7 +31,12 @@ struct AttnShape {
 // query head h reading key head h / G, G = H / Hk. The forward packs several
 // heads of a group into one 128-row Q tile (row = token * P + head), see
 // QTile.
-constexpr int kFixed = 0, kPacked = 1, kGrouped = 2;
+//
+// Shared-prefix layout (kShared, forward only): the "tokens" of a Q tile are
+// the sequences behind one prefix (one query each), its keys a range of the
+// prefix's pages; partial results go to the decoding step's workspace.
+constexpr int kFixed = 0, kPacked = 1, kGrouped = 2, kShared = 3;
+constexpr bool tile_of_heads(int layout) { return layout == kGrouped || layout == kShared; }
 
 struct Packing {
   int varlen;
@@ -99,10 +104,32 @@ struct QTile {
   int P, tok;
 };
 
+// One decoding step of sequences that share prefixes (decode_shared.cu).
+struct SharedArgs {
+  const void* q;            // bf16 [B, H, D]
+  void* o;                  // bf16 [B, H, D]
+  float* lse;               // fp32 [B, H], natural log
+  const int* prefix_table;  // int32 [P, max_prefix_blocks]
+  const int* prefix_lens;   // int32 [P], clamped to [0, max_prefix_len]
+  const int* cu_seqs;       // int32 [P + 1]: sequences of each prefix, at most max_group
+  const int* block_table;   // int32 [B, max_blocks]
+  const int* seq_lens;      // int32 [B], clamped to [0, max_seq_len]
+  int P, B, H, Hk, D;
+  int block_size, num_blocks, max_prefix_blocks, max_blocks, max_group, max_prefix_len, max_seq_len;
+  // The plan (api.cu): key ranges of `chunk` keys, `splits` of them per row,
+  // and row blocks of 64, of the prefix part and of the sequences' own part.
+  int prefix_chunk, prefix_splits, prefix_blocks, seq_chunk, seq_splits, seq_blocks;
+  int prefix_tiles;         // 1: the prefix part runs in 128-row tensor-core tiles (decode_prefix.cu)
+  float scale_log2;         // scale * log2(e)
+  float* part_o;            // workspace fp32 [B*H, prefix_splits + seq_splits, D], normalised
+  float* part_lse;          // workspace fp32 [B*H, prefix_splits + seq_splits], base 2
+};
+
 struct FwdArgs {
   AttnShape s;
   Packing pk;
-  QTile qt;              // grouped layout only
+  QTile qt;              // grouped layouts only
+  SharedArgs dec;        // shared-prefix layout only
   const int* kv_lens;    // device [B] or nullptr (fixed layout only)
   void* o;               // bf16 [B,H,N,D]
   float* lse;            // fp32 [B,H,N], natural log
@@ -174,25 +201,12 @@ struct LaunchMarks {
   cudaEvent_t stop[3];
 };
 
-// One decoding step of sequences that share prefixes (decode_shared.cu).
-struct SharedArgs {
-  const void* q;            // bf16 [B, H, D]
-  void* o;                  // bf16 [B, H, D]
-  float* lse;               // fp32 [B, H], natural log
-  const int* prefix_table;  // int32 [P, max_prefix_blocks]
-  const int* prefix_lens;   // int32 [P], clamped to [0, max_prefix_len]
-  const int* cu_seqs;       // int32 [P + 1]: sequences of each prefix, at most max_group
-  const int* block_table;   // int32 [B, max_blocks]
-  const int* seq_lens;      // int32 [B], clamped to [0, max_seq_len]
-  int P, B, H, Hk, D;
-  int block_size, num_blocks, max_prefix_blocks, max_blocks, max_group, max_prefix_len, max_seq_len;
-  // The plan (api.cu): key ranges of `chunk` keys, `splits` of them per row,
-  // and row blocks of 64, of the prefix part and of the sequences' own part.
-  int prefix_chunk, prefix_splits, prefix_blocks, seq_chunk, seq_splits, seq_blocks;
-  float scale_log2;         // scale * log2(e)
-  float* part_o;            // workspace fp32 [B*H, prefix_splits + seq_splits, D], normalised
-  float* part_lse;          // workspace fp32 [B*H, prefix_splits + seq_splits], base 2
-};
+// The prefix part of that step in tensor-core tiles: Q [B, H, D] in boxes of
+// the tile, K and V in boxes of 64 tokens.
+cudaError_t launch_decode_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const SharedArgs& a, QTile qt, cudaStream_t stream);
+cudaError_t set_decode_prefix_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
+int take_decode_prefix_status();
 cudaError_t launch_decode_shared(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                                  cudaStream_t stream, const LaunchMarks* marks);
 cudaError_t set_decode_shared_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
@@ -216,6 +230,12 @@ struct NormRopeArgs {
 constexpr int kNormRopeMaxCtas = 152 * 4;  // of the backward: one row of partial weight gradients each
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, cudaStream_t stream);
+
+// Sequences [first, first + n) behind prefix p of a shared-prefix step.
+__device__ __forceinline__ void prefix_seqs(const SharedArgs& a, int p, int& first, int& n) {
+  first = min(max(a.cu_seqs[p], 0), a.B);
+  n = min(max(min(a.cu_seqs[p + 1], a.B) - first, 0), a.max_group);
+}
 
 // Key limit of batch b: keys c >= limit are masked (clamped to [0, N]).
 __device__ __forceinline__ int key_limit(const int* kv_lens, int b, int N) {

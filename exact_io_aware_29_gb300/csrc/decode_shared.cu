@@ -86,18 +86,12 @@ struct SharedItem {
   const int* table;        // pages of the keys
 };
 
-// Sequences [first, first + n) of prefix p.
-__device__ __forceinline__ void prefix_seqs(const SharedArgs& a, int p, int& first, int& n) {
-  first = min(max(a.cu_seqs[p], 0), a.B);
-  n = min(max(min(a.cu_seqs[p + 1], a.B) - first, 0), a.max_group);
-}
-
 // False if item `id` has nothing to do.
 template <int D>
 __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedItem& it) {
   using C = SharedCfg<D>;
   const int G = a.H / a.Hk;
-  const int n_prefix_items = a.P * a.Hk * a.prefix_blocks * a.prefix_splits;
+  const int n_prefix_items = a.prefix_tiles ? 0 : a.P * a.Hk * a.prefix_blocks * a.prefix_splits;
   if (id < n_prefix_items) {
     const int split = id % a.prefix_splits;
     int x = id / a.prefix_splits;
@@ -145,8 +139,16 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::STAGES);
 
   if (threadIdx.x == 0) griddep_launch_dependents();
+  // With the prefix part in a kernel of its own before this one (launched
+  // programmatically, so that the two overlap), this grid must not end before
+  // that one: the kernel that joins the parts waits for this grid only. Its
+  // last CTA sees to that.
+  const bool waits = a.prefix_tiles && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0;
   SharedItem it;
-  if (!shared_item<D>(a, blockIdx.x, it)) return;  // the whole CTA
+  if (!shared_item<D>(a, blockIdx.x, it)) {  // the whole CTA
+    if (waits) griddep_wait();
+    return;
+  }
   const int ntiles = (it.c1 - it.c0 + C::TK - 1) / C::TK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
     *reinterpret_cast<float4*>(a.part_o + at * D + c) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (c == 0) a.part_lse[at] = sum > 0.f ? M + log2f(sum) : -INFINITY;
   }
+  if (waits) griddep_wait();
 }
 
 // Joins the parts of each row (sequence, head), prefix splits before own
@@ -398,14 +401,14 @@ static cudaError_t launch_shared_t(const CUtensorMap& tk, const CUtensorMap& tv,
   auto kern = fa_decode_shared_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(a.P) * a.Hk * a.prefix_blocks * a.prefix_splits +
+  const long long items = (a.prefix_tiles ? 0 : static_cast<long long>(a.P) * a.Hk * a.prefix_blocks * a.prefix_splits) +
                           static_cast<long long>(a.B) * a.Hk * a.seq_blocks * a.seq_splits;
   const long long rows = static_cast<long long>(a.B) * a.H;
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   mark(marks, true, 0, stream);
-  kern<<<static_cast<unsigned>(items), C::THREADS, C::SMEM_BYTES, stream>>>(tk, tv, a);
+  e = launch_maybe_pdl(kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM_BYTES, stream,
+                       a.prefix_tiles && marks == nullptr, tk, tv, a);
   mark(marks, false, 0, stream);
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   mark(marks, true, 1, stream);
   e = launch_maybe_pdl(fa_decode_shared_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,

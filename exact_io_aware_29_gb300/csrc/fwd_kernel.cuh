@@ -296,19 +296,55 @@ struct FwdCta {
   int q0, bh, hh, klim, n_max;
   int kvh;     // key head
   int tok;     // query tokens per tile (the tile's rows, over P heads when grouped)
+  int key0, slot;    // shared-prefix layout: the CTA's first key of the prefix, its partial's index,
+  const int* table;  // and the prefix's pages
   int own;     // bit t: this CTA computes and writes tile t (both, unless the pair is split)
   int n_t[2];  // key blocks each Q tile visits (fully masked blocks are skipped)
   SeqView sv;
   uint32_t tmem;
 };
 
+// Shared-prefix layout: CTAs that read the same keys (the row tiles and heads
+// of one key range) are neighbours in the grid.
+template <int D>
+__device__ __forceinline__ FwdCta fwd_cta_shared(const FwdArgs& args) {
+  using C = FwdCfg<D>;
+  const SharedArgs& a = args.dec;
+  const int cols = a.H / args.qt.P, n_pairs = (a.max_group + 2 * args.qt.tok - 1) / (2 * args.qt.tok);
+  FwdCta c;
+  c.tok = args.qt.tok;
+  int x = blockIdx.x;
+  const int pair = x % n_pairs;
+  x /= n_pairs;
+  c.hh = x % cols * args.qt.P;
+  c.kvh = c.hh / (a.H / a.Hk);
+  x /= cols;
+  const int p = x % a.P;
+  c.slot = x / a.P;
+  c.bh = 0;
+  c.q0 = pair * 2 * c.tok;
+  prefix_seqs(a, p, c.sv.q_start, c.sv.Lq);
+  c.table = a.prefix_table + static_cast<size_t>(p) * a.max_prefix_blocks;
+  c.key0 = c.slot * a.prefix_chunk;
+  c.sv.k_start = c.sv.shift = 0;
+  const int L = min(max(a.prefix_lens[p], 0), a.max_prefix_len);
+  c.sv.Lk = c.klim = max(0, min(L - c.key0, a.prefix_chunk));
+  if (c.klim == 0) c.sv.Lq = 0;  // no keys: nothing to write either
+  c.own = 3;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) c.n_t[t] = c.q0 + t * c.tok < c.sv.Lq ? (c.klim + C::BN - 1) / C::BN : 0;
+  c.n_max = max(c.n_t[0], c.n_t[1]);
+  return c;
+}
+
 template <int D, bool CAUSAL, int LAYOUT>
 __device__ __forceinline__ FwdCta fwd_cta(const FwdArgs& args) {
+  if constexpr (LAYOUT == kShared) return fwd_cta_shared<D>(args);
   using C = FwdCfg<D>;
   const AttnShape& sh = args.s;
   FwdCta c;
-  c.tok = LAYOUT == kGrouped ? args.qt.tok : C::BM;
-  const int heads = LAYOUT == kGrouped ? sh.H / args.qt.P : sh.H;  // Q tile columns per sequence
+  c.tok = tile_of_heads(LAYOUT) ? args.qt.tok : C::BM;
+  const int heads = tile_of_heads(LAYOUT) ? sh.H / args.qt.P : sh.H;  // Q tile columns per sequence
   const int BH = sh.B * heads;
   const int n_pairs = (sh.N + 2 * c.tok - 1) / (2 * c.tok);
   // The grid runs in groups of heads whose K and V fit the L2 together (every
@@ -333,7 +369,7 @@ __device__ __forceinline__ FwdCta fwd_cta(const FwdArgs& args) {
   c.bh = group * G + r_in % gsize;
   c.hh = c.bh % heads;
   c.kvh = c.hh;
-  if (LAYOUT == kGrouped) {
+  if (tile_of_heads(LAYOUT)) {
     c.hh *= args.qt.P;  // the tile's first head
     c.kvh = c.hh / (sh.H / sh.Hk);
   }
@@ -355,7 +391,7 @@ __device__ __forceinline__ FwdCta fwd_cta(const FwdArgs& args) {
 // Query row (token) of row rr of a Q tile that starts at row_start.
 template <int LAYOUT>
 __device__ __forceinline__ int fwd_row(const FwdArgs& args, int row_start, int rr) {
-  return row_start + (LAYOUT == kGrouped ? rr / args.qt.P : rr);
+  return row_start + (tile_of_heads(LAYOUT) ? rr / args.qt.P : rr);
 }
 
 // TMA: ring positions g0 + i0 .. g0 + i1 - 1 (even offsets K_(i/2), odd
@@ -363,13 +399,26 @@ __device__ __forceinline__ int fwd_row(const FwdArgs& args, int row_start, int r
 // Returns the ring position after the last load issued (g0 + i1 unless a wait
 // gave up).
 template <int D, int LAYOUT>
-__device__ __forceinline__ int fwd_load_kv_range(const FwdShared<D>& sm, const FwdCta& c, const CUtensorMap* tmK,
-                                                 const CUtensorMap* tmV, int g0, int i0, int i1) {
+__device__ __forceinline__ int fwd_load_kv_range(const FwdArgs& args, const FwdShared<D>& sm, const FwdCta& c,
+                                                 const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int i0,
+                                                 int i1) {
   using C = FwdCfg<D>;
+  int z2[2] = {0, 0};  // shared-prefix layout: pool rows of the block's two 64-key halves
   for (int idx = i0; idx < i1; ++idx) {
     const int g = g0 + idx;
     const int slot = g % C::STAGES;
     const int use = g / C::STAGES;
+    if (LAYOUT == kShared && (idx == i0 || !(idx & 1))) {
+      // K_j and V_j lie in the same pages. Keys past the range and block ids
+      // outside the pool read as zeros (TMA fills outside the tensor).
+      const SharedArgs& a = args.dec;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rel = (idx >> 1) * C::BN + h * 64, key = c.key0 + rel, page = key / a.block_size;
+        const int phys = rel < c.klim ? c.table[page] : -1;
+        z2[h] = phys < 0 || phys >= a.num_blocks ? -64 : phys * a.block_size + (key - page * a.block_size);
+      }
+    }
     if (use > 0 && !mbar_wait(&sm.kv_empty[slot], (use - 1) & 1, sm.abort_flag)) return g;
     mbar_arrive_expect_tx(&sm.kv_full[slot], C::KV_BYTES);
     const CUtensorMap* tm = (idx & 1) ? tmV : tmK;
@@ -377,8 +426,17 @@ __device__ __forceinline__ int fwd_load_kv_range(const FwdShared<D>& sm, const F
     const int row = (idx >> 1) * C::BN;
     const int y = LAYOUT != kFixed ? c.kvh : row;
     const int z = LAYOUT != kFixed ? c.sv.k_start + row : c.bh;
+    if constexpr (LAYOUT == kShared) {
 #pragma unroll
-    for (int cc = 0; cc < C::CHUNKS; ++cc) tma_load_3d(dst + cc * C::SUB_BYTES, tm, &sm.kv_full[slot], cc * 64, y, z);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int cc = 0; cc < C::CHUNKS; ++cc)
+          tma_load_3d(dst + cc * C::SUB_BYTES + h * (64 * 128), tm, &sm.kv_full[slot], cc * 64, c.kvh, z2[h]);
+      }
+    } else {
+#pragma unroll
+      for (int cc = 0; cc < C::CHUNKS; ++cc) tma_load_3d(dst + cc * C::SUB_BYTES, tm, &sm.kv_full[slot], cc * 64, y, z);
+    }
   }
   return g0 + i1;
 }
@@ -387,9 +445,9 @@ __device__ __forceinline__ int fwd_load_kv_range(const FwdShared<D>& sm, const F
 // ... Returns the ring position after the last load issued (g0 + 2 n unless a
 // wait gave up).
 template <int D, int LAYOUT>
-__device__ __forceinline__ int fwd_load_kv(const FwdShared<D>& sm, const FwdCta& c, const CUtensorMap* tmK,
-                                           const CUtensorMap* tmV, int g0, int n) {
-  return fwd_load_kv_range<D, LAYOUT>(sm, c, tmK, tmV, g0, 0, 2 * n);
+__device__ __forceinline__ int fwd_load_kv(const FwdArgs& args, const FwdShared<D>& sm, const FwdCta& c,
+                                           const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int n) {
+  return fwd_load_kv_range<D, LAYOUT>(args, sm, c, tmK, tmV, g0, 0, 2 * n);
 }
 
 // Wait for the ring copies in flight, the last STAGES positions before
@@ -573,8 +631,30 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgs& args, const FwdCta&
                                               float m_used, float l, float unscale, int rr) {
   const bool valid = r < c.sv.Lq && (LAYOUT != kGrouped || rr < args.qt.tok * args.qt.P);
   // Flattened query head of the row (grouped: row rr of the tile is head hh + rr % P).
-  const int bh = LAYOUT == kGrouped ? c.hh + rr % args.qt.P : c.bh;
+  const int bh = tile_of_heads(LAYOUT) ? c.hh + rr % args.qt.P : c.bh;
   const float inv = (l > 0.f) ? 1.f / l : 0.f;
+  if constexpr (LAYOUT == kShared) {
+    // A partial result: normalised O in fp32 and the base-2 log of the sum.
+    const size_t at = (static_cast<size_t>(c.sv.q_start + r) * args.dec.H + bh) *
+                          (args.dec.prefix_splits + args.dec.seq_splits) + c.slot;
+    float omax = 0.f;
+#pragma unroll
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t o[32];
+      tmem_ld32(tO + cc * 32, o);
+      tmem_wait_ld();
+      float4* out = reinterpret_cast<float4*>(args.dec.part_o + at * D + cc * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x[4] = {__uint_as_float(o[4 * i]) * inv * unscale, __uint_as_float(o[4 * i + 1]) * inv * unscale,
+                            __uint_as_float(o[4 * i + 2]) * inv * unscale, __uint_as_float(o[4 * i + 3]) * inv * unscale};
+        omax = max3_nan_abs(max3_nan_abs(omax, x[0], x[1]), x[2], x[3]);
+        if (valid) out[i] = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    if (valid) args.dec.part_lse[at] = (l > 0.f) ? m_used + log2f(l) - 7.0f : -INFINITY;
+    return omax;
+  }
   // Output row r of this sequence: [B,H,N,d] or packed [total,H,d]; LSE
   // [B,H,N] or [H,total].
   uint4* orow =
@@ -631,8 +711,8 @@ __device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtenso
   const int g_scan = 2 * c.n_max, g_pass = g_scan + 2 * n_r;
   if (warp == 0) {
     if (lane == 0 && !g_test_drop_loads) {
-      int loads = fwd_load_kv<D, LAYOUT>(sm, c, tmK, tmV, g_scan, n_r);
-      if (loads == g_pass) loads = fwd_load_kv<D, LAYOUT>(sm, c, tmK, tmV, g_pass, n_r);
+      int loads = fwd_load_kv<D, LAYOUT>(args, sm, c, tmK, tmV, g_scan, n_r);
+      if (loads == g_pass) loads = fwd_load_kv<D, LAYOUT>(args, sm, c, tmK, tmV, g_pass, n_r);
       fwd_drain_loads<D>(sm, loads);
     }
   } else if (warp == 1) {
@@ -729,7 +809,7 @@ __global__ void __launch_bounds__(384, 1)
     if (c.n_t[t] > 0) {
       // A grouped tile's box is [tok tokens][P heads] rows of 128 bytes.
       mbar_arrive_expect_tx(&sm.q_full[t],
-                            LAYOUT == kGrouped ? args.qt.tok * args.qt.P * (C::CHUNKS * 128) : C::Q_BYTES);
+                            tile_of_heads(LAYOUT) ? args.qt.tok * args.qt.P * (C::CHUNKS * 128) : C::Q_BYTES);
       const int row = c.q0 + t * c.tok;
       const int y = LAYOUT != kFixed ? c.hh : row;
       const int z = LAYOUT != kFixed ? c.sv.q_start + row : c.bh;
@@ -748,9 +828,9 @@ __global__ void __launch_bounds__(384, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       load_q(0);
-      fwd_load_kv_range<D, LAYOUT>(sm, c, &tmK, &tmV, 0, 0, min(1, early));
+      fwd_load_kv_range<D, LAYOUT>(args, sm, c, &tmK, &tmV, 0, 0, min(1, early));
       load_q(1);
-      fwd_load_kv_range<D, LAYOUT>(sm, c, &tmK, &tmV, 0, min(1, early), early);
+      fwd_load_kv_range<D, LAYOUT>(args, sm, c, &tmK, &tmV, 0, min(1, early), early);
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm.smem + C::OFF_BAR);
     for (int i = 2 + C::STAGES; i < C::NUM_BARS; ++i) mbar_init(&bars[i], 1);  // after q_full, kv_full
@@ -779,7 +859,7 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
     if (lane == 0 && !g_test_drop_loads) {
-      fwd_drain_loads<D>(sm, fwd_load_kv_range<D, LAYOUT>(sm, c, &tmK, &tmV, 0, early, 2 * c.n_max));
+      fwd_drain_loads<D>(sm, fwd_load_kv_range<D, LAYOUT>(args, sm, c, &tmK, &tmV, 0, early, 2 * c.n_max));
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (c.n_t[t] > 0) mbar_wait_drain(&sm.q_full[t], 0);
@@ -888,8 +968,8 @@ static cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, co
   auto kern = fa_fwd_kernel<D, CAUSAL, LAYOUT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int tok = LAYOUT == kGrouped ? a.qt.tok : C::BM;                    // query tokens per tile
-  const int BH = a.s.B * (LAYOUT == kGrouped ? a.s.H / a.qt.P : a.s.H);  // tile columns
+  const int tok = tile_of_heads(LAYOUT) ? a.qt.tok : C::BM;                    // query tokens per tile
+  const int BH = a.s.B * (tile_of_heads(LAYOUT) ? a.s.H / a.qt.P : a.s.H);  // tile columns
   // Heads per group: at most as many as keep their K and V (bf16, 4 d bytes
   // per key row; the longest sequence for a packed batch) within half the L2,
   // the rest of it left to the Q tiles and the outputs streaming through;
@@ -898,7 +978,7 @@ static cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, co
     const long long per_head = static_cast<long long>(std::max(a.s.Nk, 1)) * D * 4;
     const long long l2 = current_l2_bytes();
     // Grouped: the G / P tile columns of a key head read the same K and V.
-    const long long share = LAYOUT == kGrouped ? a.s.H / a.s.Hk / a.qt.P : 1;
+    const long long share = tile_of_heads(LAYOUT) ? a.s.H / a.s.Hk / a.qt.P : 1;
     const long long g = l2 > 0 ? (l2 / 2) / per_head * share : BH;
     a.heads_per_group = balanced_heads_per_group(BH, g);
   }
