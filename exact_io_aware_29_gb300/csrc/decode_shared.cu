@@ -341,15 +341,18 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
 }
 
 // Joins the parts of each row (sequence, head), prefix splits before own
-// splits: O = sum of 2^(lse_i - M) O_i over the sum of the weights. One warp
-// per row.
+// splits: O = sum of 2^(lse_i - M) O_i over the sum of the weights. One CTA
+// per row: its four warps take every fourth part, then sum theirs in shared
+// memory. How many parts there are follows from the lengths and is worked out
+// before the wait for the kernels that write them (this one is launched
+// programmatically); after it there are two dependent reads, the sums and the
+// parts. (One warp per row, part after part: 14 us for 64 rows of 20 parts.)
 template <int D>
-__global__ void __launch_bounds__(256) fa_decode_shared_join_kernel(const SharedArgs a) {
+__global__ void __launch_bounds__(128) fa_decode_shared_join_kernel(const SharedArgs a) {
   constexpr int CPL = D / 32;  // columns per lane
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.B) * a.H) return;
-  const int b = static_cast<int>(row / a.H);
+  __shared__ float red[4][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / a.H;
   // The prefix of sequence b: the last p with cu_seqs[p] <= b.
   int lo = 0, hi = a.P;
   while (lo < hi) {
@@ -366,9 +369,9 @@ __global__ void __launch_bounds__(256) fa_decode_shared_join_kernel(const Shared
   const int L = min(max(a.seq_lens[b], 0), a.max_seq_len);
   const int np = (Lp + a.prefix_chunk - 1) / a.prefix_chunk;
   const int n = np + (L + a.seq_chunk - 1) / a.seq_chunk;
-  const size_t at0 = static_cast<size_t>(row) * (a.prefix_splits + a.seq_splits);
+  const size_t at0 = static_cast<size_t>(blockIdx.x) * (a.prefix_splits + a.seq_splits);
   auto part = [&](int i) { return at0 + (i < np ? i : a.prefix_splits + i - np); };
-  griddep_wait();  // the parts come from the kernel before
+  griddep_wait();
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_lse[part(i)]);
 #pragma unroll
@@ -376,21 +379,43 @@ __global__ void __launch_bounds__(256) fa_decode_shared_join_kernel(const Shared
   float sum = 0.f, acc[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
-  if (M > -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const size_t at = part(i);
-      const float w = ex2(a.part_lse[at] - M);
-      sum += w;
-#pragma unroll
-      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(w, a.part_o[at * D + lane * CPL + k], acc[k]);
+  for (int i0 = 0; i0 < n && M > -INFINITY; i0 += 128) {
+    // This warp's parts i0 + warp + 4 j, j < 32: lane j holds the weight of the j-th.
+    const int mine = i0 + warp + 4 * lane;
+    const float w = mine < n ? ex2(a.part_lse[part(mine)] - M) : 0.f;
+    const int count = min(32, (n - i0 - warp + 3) / 4);
+#pragma unroll 8
+    for (int j = 0; j < count; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float* src = a.part_o + part(i0 + warp + 4 * j) * D + lane * CPL;
+      sum += wj;
+      if constexpr (CPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(wj, x.x, acc[0]), acc[1] = fmaf(wj, x.y, acc[1]);
+        acc[2] = fmaf(wj, x.z, acc[2]), acc[3] = fmaf(wj, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(wj, x.x, acc[0]), acc[1] = fmaf(wj, x.y, acc[1]);
+      }
     }
   }
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) red[warp][lane * CPL + k] = acc[k];
+  if (lane == 0) red[warp][D] = sum;
+  __syncthreads();
+  if (warp > 0) return;
+  sum = red[0][D];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    sum += red[w][D];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) acc[k] += red[w][lane * CPL + k];
+  }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + lane * CPL);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + static_cast<size_t>(blockIdx.x) * D + lane * CPL);
 #pragma unroll
   for (int k = 0; k < CPL; k += 2) out[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0) a.lse[row] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[blockIdx.x] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D>
@@ -404,14 +429,14 @@ static cudaError_t launch_shared_t(const CUtensorMap& tk, const CUtensorMap& tv,
   const long long items = (a.prefix_tiles ? 0 : static_cast<long long>(a.P) * a.Hk * a.prefix_blocks * a.prefix_splits) +
                           static_cast<long long>(a.B) * a.Hk * a.seq_blocks * a.seq_splits;
   const long long rows = static_cast<long long>(a.B) * a.H;
-  if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (items > 0x7fffffffLL || rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   mark(marks, true, 0, stream);
   e = launch_maybe_pdl(kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM_BYTES, stream,
                        a.prefix_tiles && marks == nullptr, tk, tv, a);
   mark(marks, false, 0, stream);
   if (e != cudaSuccess) return e;
   mark(marks, true, 1, stream);
-  e = launch_maybe_pdl(fa_decode_shared_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
+  e = launch_maybe_pdl(fa_decode_shared_join_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(128), 0,
                        stream, marks == nullptr, a);
   mark(marks, false, 1, stream);
   return e;

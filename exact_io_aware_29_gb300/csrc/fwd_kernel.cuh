@@ -629,7 +629,7 @@ __device__ __forceinline__ bool fwd_softmax_pass(const FwdShared<D>& sm, const F
 template <int D, int LAYOUT>
 __device__ __forceinline__ float fwd_epilogue(const FwdArgs& args, const FwdCta& c, int r, uint32_t tO, bool have_o,
                                               float m_used, float l, float unscale, int rr) {
-  const bool valid = r < c.sv.Lq && (LAYOUT != kGrouped || rr < args.qt.tok * args.qt.P);
+  const bool valid = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || rr < args.qt.tok * args.qt.P);
   // Flattened query head of the row (grouped: row rr of the tile is head hh + rr % P).
   const int bh = tile_of_heads(LAYOUT) ? c.hh + rr % args.qt.P : c.bh;
   const float inv = (l > 0.f) ? 1.f / l : 0.f;
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(384, 1)
       // Range check: a row that needs the bf16 pass flags its tile (what was
       // written is then overwritten).
       // Rows of a grouped tile past its tok * P hold nothing.
-      const bool real = r < c.sv.Lq && (LAYOUT != kGrouped || wq * 32 + lane < args.qt.tok * args.qt.P);
+      const bool real = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || wq * 32 + lane < args.qt.tok * args.qt.P);
       if (ok && real && row_needs_bf16_pass(omax, l)) atomicOr(const_cast<uint32_t*>(sm.redo), 1u << t);
     }
   }
