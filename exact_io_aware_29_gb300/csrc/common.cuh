@@ -260,24 +260,38 @@ inline int balanced_heads_per_group(long long bh, long long g_max) {
   return static_cast<int>((bh + groups - 1) / groups);
 }
 
-// Launch ``kern`` on ``stream``, with programmatic stream serialization when
-// ``pdl`` (the kernel may then start before the previous kernel on the stream
-// has finished, and must call griddepcontrol.wait before reading its
-// results). Returns the launch's error.
+// Launch ``kern`` on ``stream`` in clusters of ``cluster`` CTAs, with
+// programmatic stream serialization when ``pdl`` (the kernel may then start
+// before the previous kernel on the stream has finished, and must call
+// griddepcontrol.wait before reading its results). Returns the launch's error.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_maybe_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                    bool pdl, Args&&... args) {
+inline cudaError_t launch_cluster_maybe_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                            cudaStream_t stream, bool pdl, int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = n > 0 ? attr : nullptr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_maybe_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                    bool pdl, Args&&... args) {
+  return launch_cluster_maybe_pdl(kern, grid, block, smem, stream, pdl, 1, std::forward<Args>(args)...);
 }
 
 // Host launchers (defined in fwd.cu / bwd.cu). Return cudaError_t of the launch.

@@ -84,9 +84,11 @@ struct SharedItem {
   int kvh, c0, c1;         // key head, key range
   int slot;                // partial index of every row
   const int* table;        // pages of the keys
+  int phys;                // block id of the first page
 };
 
-// False if item `id` has nothing to do.
+// False if item `id` has nothing to do. What it reads (offsets, length, first
+// block id) it reads in one go: a short item's time is made of such latencies.
 template <int D>
 __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedItem& it) {
   using C = SharedCfg<D>;
@@ -100,14 +102,15 @@ __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedI
     it.kvh = x % a.Hk;
     const int p = x / a.Hk;
     int n;
+    it.c0 = split * a.prefix_chunk;
+    it.table = a.prefix_table + static_cast<size_t>(p) * a.max_prefix_blocks;
+    it.phys = it.table[it.c0 / a.block_size];  // c0 < max_prefix_len: inside the row
+    const int L = min(max(a.prefix_lens[p], 0), a.max_prefix_len);
     prefix_seqs(a, p, it.seq0, n);
     it.row0 = blk * C::ROWS;
     it.rows = min(n * G - it.row0, C::ROWS);
-    const int L = min(max(a.prefix_lens[p], 0), a.max_prefix_len);
-    it.c0 = split * a.prefix_chunk;
     it.c1 = min(L, it.c0 + a.prefix_chunk);
     it.slot = split;
-    it.table = a.prefix_table + static_cast<size_t>(p) * a.max_prefix_blocks;
   } else {
     id -= n_prefix_items;
     const int split = id % a.seq_splits;
@@ -118,11 +121,12 @@ __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedI
     it.seq0 = x / a.Hk;
     it.row0 = blk * C::ROWS;
     it.rows = min(G - it.row0, C::ROWS);
-    const int L = min(max(a.seq_lens[it.seq0], 0), a.max_seq_len);
     it.c0 = split * a.seq_chunk;
+    it.table = a.block_table + static_cast<size_t>(it.seq0) * a.max_blocks;
+    it.phys = it.table[it.c0 / a.block_size];
+    const int L = min(max(a.seq_lens[it.seq0], 0), a.max_seq_len);
     it.c1 = min(L, it.c0 + a.seq_chunk);
     it.slot = a.prefix_splits + split;
-    it.table = a.block_table + static_cast<size_t>(it.seq0) * a.max_blocks;
   }
   return it.rows > 0 && it.c1 > it.c0;
 }
@@ -151,49 +155,21 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
   }
   const int ntiles = (it.c1 - it.c0 + C::TK - 1) / C::TK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::CWARPS);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-
-  if (warp == C::CWARPS) {
-    // ------------------------------------------------------------ TMA warp
-    if (lane == 0 && !g_test_drop_loads) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      int issued = 0;
-      for (int t = 0; t < ntiles; ++t) {
-        const int s = t % C::STAGES, use = t / C::STAGES;
-        if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, abort_flag)) break;
-        const int key = it.c0 + t * C::TK;
-        const int page = key / a.block_size;
-        const int phys = it.table[page];
-        // Out-of-range block ids read as zeros (TMA fills outside the pool).
-        const int row = (phys < 0 || phys >= a.num_blocks) ? -C::TK : phys * a.block_size + (key - page * a.block_size);
-        uint8_t* st = smem + s * C::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+  // Tile t into its stage, from block `phys` (the page of key c0 + 64 t).
+  // Out-of-range block ids read as zeros (TMA fills outside the pool).
+  auto issue = [&](int t, int phys) {
+    const int key = it.c0 + t * C::TK, s = t % C::STAGES;
+    const int row = (phys < 0 || phys >= a.num_blocks) ? -C::TK : phys * a.block_size + key % a.block_size;
+    uint8_t* st = smem + s * C::STAGE_BYTES;
+    mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
 #pragma unroll
-        for (int c = 0; c < C::BOXES; ++c) {
-          tma_load_3d(st + c * C::BOX_BYTES, &tmK, &full[s], c * 64, it.kvh, row);
-          tma_load_3d(st + C::TILE_BYTES + c * C::BOX_BYTES, &tmV, &full[s], c * 64, it.kvh, row);
-        }
-        ++issued;
-      }
-      // Do not leave with copies in flight (matters only after an abort, when
-      // the consumers stopped waiting; every issued copy lands).
-      for (int t = max(0, issued - C::STAGES); t < issued; ++t) mbar_wait_drain(&full[t % C::STAGES], (t / C::STAGES) & 1);
+    for (int c = 0; c < C::BOXES; ++c) {
+      tma_load_3d(st + c * C::BOX_BYTES, &tmK, &full[s], c * 64, it.kvh, row);
+      tma_load_3d(st + C::TILE_BYTES + c * C::BOX_BYTES, &tmV, &full[s], c * 64, it.kvh, row);
     }
-    return;
-  }
-
-  // -------------------------------------------------------- consumer warps
-  // nb 16-row blocks (1, 2 or 4): warp w works on block w % nb and on every
-  // (4 / nb)-th 16-key part of a tile from part w / nb on.
+  };
+  // nb 16-row blocks (1, 2 or 4): consumer warp w works on block w % nb and on
+  // every (4 / nb)-th 16-key part of a tile from part w / nb on.
   const int G = a.H / a.Hk;
   const int nb = it.rows <= 16 ? 1 : (it.rows <= 32 ? 2 : 4);
   const int blk = warp % nb, part0 = warp / nb, step = C::CWARPS / nb;
@@ -204,7 +180,17 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
   };
   const int gr = lane >> 2, gc = (lane & 3) * 2;  // this lane's rows gr, gr + 8 and columns gc, gc + 1
   uint32_t qf[D / 16][4];
-  {
+  if (warp == C::CWARPS) {
+    if (lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], C::CWARPS);
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+      if (!g_test_drop_loads) issue(0, it.phys);  // the first copy overlaps the rest of the set-up
+    }
+  } else {
     const long long r0 = q_index(blk * 16 + gr), r1 = q_index(blk * 16 + gr + 8);
     const uint16_t* q = static_cast<const uint16_t*>(a.q);
 #pragma unroll
@@ -216,6 +202,26 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
       qf[kk][3] = r1 < 0 ? 0u : *reinterpret_cast<const uint32_t*>(q + r1 * D + c + 8);
     }
   }
+  __syncthreads();
+
+  if (warp == C::CWARPS) {
+    // ------------------------------------------------------------ TMA warp
+    if (lane == 0 && !g_test_drop_loads) {
+      int issued = 1;
+      for (int t = 1; t < ntiles; ++t) {
+        const int phys = it.table[(it.c0 + t * C::TK) / a.block_size];
+        if (t >= C::STAGES && !mbar_wait(&empty[t % C::STAGES], (t / C::STAGES - 1) & 1, abort_flag)) break;
+        issue(t, phys);
+        ++issued;
+      }
+      // Do not leave with copies in flight (matters only after an abort, when
+      // the consumers stopped waiting; every issued copy lands).
+      for (int t = max(0, issued - C::STAGES); t < issued; ++t) mbar_wait_drain(&full[t % C::STAGES], (t / C::STAGES) & 1);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------- consumer warps
   float o[D / 8][4];
 #pragma unroll
   for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;

@@ -61,6 +61,8 @@ CASES = [
     (24, 1, [33, 12], [33, 0]),                            # eight a tile (24 would waste rows); no keys
     (44, 4, [31, 3], [90, 3]),                             # eleven: one head a tile
     (2, 1, [1000], [1500]),                                # continued prompt over many blocks
+    (16, 8, [100 + 9 * i for i in range(20)], [100 + 9 * i for i in range(20)]),  # more key blocks than SMs
+    (4, 1, [700, 650], [700, 650]),                        # few key blocks: their pairs shared out over CTAs
 ]
 
 
