@@ -227,7 +227,7 @@ struct NormRopeArgs {
   int rows, q_slices, k_slices;  // set at launch: heads per unit of work, units per token
   float eps;
 };
-constexpr int kNormRopeMaxCtas = 152 * 4;  // of the backward: one row of partial weight gradients each
+constexpr int kNormRopeMaxCtas = 152 * 2;  // of the backward: one row of partial weight gradients each
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, cudaStream_t stream);
 
