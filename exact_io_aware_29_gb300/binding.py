@@ -248,11 +248,13 @@ def _load_torch():
     return _torch
 
 
-def _want(where, name, t, dtype, shape, dev) -> None:
-    """t must be contiguous, of this dtype and shape, on CUDA device ``dev``."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}; "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+def _want_all(where, dev, wanted) -> None:
+    """Every (name, tensor, dtype, shape): contiguous, of that dtype and shape, on CUDA device ``dev``."""
+    for name, t, dtype, shape in wanted:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                             f"cuda:{dev}; got {t.dtype} {tuple(t.shape)} on {t.device}" +
+                             ("" if t.is_contiguous() else ", strided"))
 
 
 def _cuda_index(where, t) -> int:
@@ -310,18 +312,12 @@ def _check_gqa(where, q, k, v, q_like, k_like, lse, cu_seqlens_q, cu_seqlens_k):
         raise ValueError(f"{where}: q is [total_q, H, d], k and v [total_k, H_kv, d] with H a multiple of H_kv; got "
                          f"{tuple(qs)} and {tuple(ks)}")
     total_q, H, d = qs
-    _want(where, "q", q, bf16, qs, dev)
-    _want(where, "k", k, bf16, ks, dev)
-    _want(where, "v", v, bf16, ks, dev)
-    for name, t in q_like:
-        _want(where, name, t, bf16, qs, dev)
-    for name, t in k_like:
-        _want(where, name, t, bf16, ks, dev)
-    _want(where, "lse", lse, torch.float32, (H, total_q), dev)
-    batch = cu_seqlens_q.numel() - 1
-    _want(where, "cu_seqlens_q", cu_seqlens_q, torch.int32, (batch + 1,), dev)
-    _want(where, "cu_seqlens_k", cu_seqlens_k, torch.int32, (batch + 1,), dev)
-    return dev, (batch, H, ks[1], d, total_q, ks[0])
+    n = cu_seqlens_q.numel()
+    _want_all(where, dev, (("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks),
+                           ("lse", lse, torch.float32, (H, total_q)), ("cu_seqlens_q", cu_seqlens_q, torch.int32, (n,)),
+                           ("cu_seqlens_k", cu_seqlens_k, torch.int32, (n,)),
+                           *[(name, t, bf16, qs) for name, t in q_like], *[(name, t, bf16, ks) for name, t in k_like]))
+    return dev, (n - 1, H, ks[1], d, total_q, ks[0])
 
 
 def fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
@@ -532,16 +528,11 @@ def fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_le
     B, H, d = qs
     P, prefix_width = prefix_table.shape
     width = block_table.shape[1]
-    _want(where, "q", q, bf16, qs, dev)
-    _want(where, "k_cache", k_cache, bf16, cs, dev)
-    _want(where, "v_cache", v_cache, bf16, cs, dev)
-    _want(where, "o", o, bf16, qs, dev)
-    _want(where, "lse", lse, torch.float32, (B, H), dev)
-    _want(where, "prefix_table", prefix_table, i32, (P, prefix_width), dev)
-    _want(where, "prefix_lens", prefix_lens, i32, (P,), dev)
-    _want(where, "cu_prefix_seqs", cu_prefix_seqs, i32, (P + 1,), dev)
-    _want(where, "block_table", block_table, i32, (B, width), dev)
-    _want(where, "seq_lens", seq_lens, i32, (B,), dev)
+    _want_all(where, dev, (
+        ("q", q, bf16, qs), ("k_cache", k_cache, bf16, cs), ("v_cache", v_cache, bf16, cs), ("o", o, bf16, qs),
+        ("lse", lse, torch.float32, (B, H)), ("prefix_table", prefix_table, i32, (P, prefix_width)),
+        ("prefix_lens", prefix_lens, i32, (P,)), ("cu_prefix_seqs", cu_prefix_seqs, i32, (P + 1,)),
+        ("block_table", block_table, i32, (B, width)), ("seq_lens", seq_lens, i32, (B,))))
     max_group, max_prefix_len, max_seq_len = int(max_group), int(max_prefix_len), int(max_seq_len)
     workspace, ws, ws_bytes = _workspace(where, workspace, lambda: fa_decode_shared_prefix_workspace_size(
         P, B, H, cs[2], d, max_group, max_prefix_len, max_seq_len), dev, stream)
@@ -572,7 +563,7 @@ def _heads_stride(where, name, t, T, H, d, dev) -> int:
     return st[0] if T > 1 else H * d
 
 
-def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions):
+def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, of=""):
     """(device, token strides of q and k, the C call's sizes)."""
     torch = _load_torch()
     dev = _cuda_index(where, q)
@@ -582,11 +573,11 @@ def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions):
                          f"{tuple(ks)} and {tuple(table)}")
     T, H, d = qs
     strides = _heads_stride(where, "q", q, T, H, d, dev), _heads_stride(where, "k", k, T, ks[1], d, dev)
-    _want(where, "q_weight", q_weight, torch.bfloat16, (d,), dev)
-    _want(where, "k_weight", k_weight, torch.bfloat16, (d,), dev)
-    _want(where, "cos", cos, torch.float32, table, dev)
-    _want(where, "sin", sin, torch.float32, table, dev)
-    _want(where, "positions", positions, torch.int32, (T,), dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    _want_all(where, dev, (("q_weight", q_weight, bf16, (d,)), ("k_weight", k_weight, bf16, (d,)),
+                           ("cos", cos, f32, table), ("sin", sin, f32, table),
+                           ("positions", positions, torch.int32, (T,)), (of + "q_out", q_out, bf16, qs),
+                           (of + "k_out", k_out, bf16, ks)))
     return dev, strides, (T, H, ks[1], d, 2 * table[1], table[0])
 
 
@@ -596,9 +587,7 @@ def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out,
     entry point. q and k may be strided over tokens (parts of a fused
     projection); the rotated width is 2 * cos.shape[1]."""
     where = "fa_qk_norm_rope"
-    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions)
-    _want(where, "q_out", q_out, _torch.bfloat16, q.shape, dev)
-    _want(where, "k_out", k_out, _torch.bfloat16, k.shape, dev)
+    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
     _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
           sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *sizes, *strides, float(eps),
           int(bool(interleaved)))
@@ -622,13 +611,11 @@ def fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, d
     """Backward of fa_qk_norm_rope; same semantics as the C entry point. dq
     and dk may be strided over tokens, like q and k."""
     where = "fa_qk_norm_rope_bwd"
-    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions)
+    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, "d")
     T, H, H_kv, d = sizes[:4]
-    _want(where, "dq_out", dq_out, _torch.bfloat16, q.shape, dev)
-    _want(where, "dk_out", dk_out, _torch.bfloat16, k.shape, dev)
     out_strides = _heads_stride(where, "dq", dq, T, H, d, dev), _heads_stride(where, "dk", dk, T, H_kv, d, dev)
-    _want(where, "dq_weight", dq_weight, _torch.float32, (d,), dev)
-    _want(where, "dk_weight", dk_weight, _torch.float32, (d,), dev)
+    _want_all(where, dev, (("dq_weight", dq_weight, _torch.float32, (d,)),
+                           ("dk_weight", dk_weight, _torch.float32, (d,))))
     workspace, ws, ws_bytes = _workspace(where, workspace,
                                          lambda: fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d), dev, stream)
     _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
