@@ -155,8 +155,9 @@ bool encode_u8(CUtensorMap* m, const void* ptr, long long dim0, long long dim1, 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Check mode: copy cu_seqlens to the host and validate them.
-int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream);
+// Check mode: copy cu_seqlens to the host and validate them (`spare`: rows of
+// no sequence may follow the last one).
+int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream, bool spare = false);
 
 bool check_mode() {
   static int mode = -1;
@@ -188,13 +189,13 @@ int check_kv_lens(const int* kv_lens, int B, int N, cudaStream_t stream) {
   return FA_OK;
 }
 
-int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream) {
+int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream, bool spare) {
   if (!check_mode()) return FA_OK;
   std::vector<int> h(batch + 1);
   cudaError_t e = cudaMemcpyAsync(h.data(), cu, sizeof(int) * (batch + 1), cudaMemcpyDeviceToHost, stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return launch_error(e);
-  if (h[0] != 0 || h[batch] != total) return FA_ERR_INVALID;
+  if (h[0] != 0 || (spare ? h[batch] > total : h[batch] != total)) return FA_ERR_INVALID;
   for (int b = 0; b < batch; ++b)
     if (h[b + 1] < h[b] || h[b + 1] - h[b] > max_len) return FA_ERR_INVALID;
   return FA_OK;
@@ -501,8 +502,8 @@ int fa_fwd_varlen_gqa(const void* q, const void* k, const void* v, void* o, floa
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
     return FA_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s);
-  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s);
+  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s, true);
+  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s, true);
   if (st != FA_OK) return st;
   st = apply_test_hooks(s);
   if (st != FA_OK) return st;
@@ -750,8 +751,8 @@ static int bwd_varlen_gqa(const void* q, const void* k, const void* v, const voi
   const size_t need = fa_bwd_workspace_size(batch, H, max_seqlen_q, d);
   if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s);
-  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s);
+  st = check_cu_seqlens(cu_seqlens_q, batch, total_q, max_seqlen_q, s, true);
+  if (st == FA_OK) st = check_cu_seqlens(cu_seqlens_k, batch, total_k, max_seqlen_k, s, true);
   if (st != FA_OK) return st;
   st = apply_test_hooks(s);
   if (st != FA_OK) return st;
