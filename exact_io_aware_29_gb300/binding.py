@@ -235,7 +235,8 @@ def attention_backward_varlen(q, k, v, o, lse, dO, cu_seqlens_q, cu_seqlens_k, m
 
 # ---------------------------------------------------------------------------
 # The grouped-head operators are called once per layer and token, where the
-# host's time counts: their checks go over each tensor once.
+# host's time counts: a call checks its tensors in one expression, and only a
+# call that fails it goes over them by name.
 # ---------------------------------------------------------------------------
 _torch = None
 
@@ -248,13 +249,15 @@ def _load_torch():
     return _torch
 
 
-def _want_all(where, dev, wanted) -> None:
-    """Every (name, tensor, dtype, shape): contiguous, of that dtype and shape, on CUDA device ``dev``."""
+def _refuse(where, dev, wanted) -> None:
+    """Raises for the first (name, tensor, dtype, shape) that is not
+    contiguous, of that dtype and shape, on CUDA device ``dev``."""
     for name, t, dtype, shape in wanted:
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                              f"cuda:{dev}; got {t.dtype} {tuple(t.shape)} on {t.device}" +
                              ("" if t.is_contiguous() else ", strided"))
+    raise ValueError(f"{where}: arguments do not fit together")
 
 
 def _cuda_index(where, t) -> int:
@@ -262,6 +265,23 @@ def _cuda_index(where, t) -> int:
     if dev < 0 or not t.is_cuda:
         raise ValueError(f"{where} needs CUDA tensors")
     return dev
+
+
+def _raw_stream(where, dev, stream):
+    """The cudaStream_t of a call on device ``dev`` (None: its current stream)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _on_device(dev, fn, *args):
+    """fn(*args) with device ``dev`` current (the library launches on the current device)."""
+    if dev == _torch._C._cuda_getDevice():
+        return fn(*args)
+    with _torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _alloc(stream, make):
@@ -274,49 +294,39 @@ def _alloc(stream, make):
         return make()
 
 
-def _workspace(where, t, need, dev, stream):
-    """The caller's workspace, or one of need() bytes: (tensor, pointer, bytes)."""
+def _workspace(where, t, dev, stream, size, *sizes):
+    """The caller's workspace, or one of size(*sizes) bytes."""
     if t is None:
-        t = _alloc(stream, lambda: _torch.empty(max(need(), 1), dtype=_torch.uint8, device=f"cuda:{dev}"))
-    elif t.get_device() != dev or not t.is_contiguous():
+        return _alloc(stream, lambda: _torch.empty(max(size(*sizes), 1), dtype=_torch.uint8, device=f"cuda:{dev}"))
+    if t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{where}: workspace must be a contiguous tensor on cuda:{dev}")
-    return t, t.data_ptr(), t.numel() * t.element_size()
+    return t
 
 
-def _call(where, dev, stream, *args) -> None:
-    """Calls the C entry point ``where`` with device ``dev`` current, on
-    ``stream`` (None: the current stream of ``dev``) as its last argument."""
-    torch = _torch
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index != dev:
-        raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
-    else:
-        raw = stream.cuda_stream
-    fn = getattr(_LIB or load_library(), where)
-    if dev == torch.cuda.current_device():
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, raw)
-    if st != FA_OK:
-        raise FaError(st, where)
-
-
-def _check_gqa(where, q, k, v, q_like, k_like, lse, cu_seqlens_q, cu_seqlens_k):
-    """Shapes of a grouped-head packed call: (device, the C call's sizes up to total_k)."""
-    torch = _load_torch()
+def _check_gqa(where, q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k):
+    """Checks what both directions of the grouped-head packed attention take:
+    (device, the C call's sizes up to total_k)."""
+    torch = _torch or _load_torch()
     dev = _cuda_index(where, q)
-    qs, ks, bf16 = q.shape, k.shape, torch.bfloat16
+    qs, ks, bf16, i32 = q.shape, k.shape, torch.bfloat16, torch.int32
     if len(qs) != 3 or len(ks) != 3 or ks[2] != qs[2] or ks[1] < 1 or qs[1] % ks[1]:
         raise ValueError(f"{where}: q is [total_q, H, d], k and v [total_k, H_kv, d] with H a multiple of H_kv; got "
                          f"{tuple(qs)} and {tuple(ks)}")
     total_q, H, d = qs
     n = cu_seqlens_q.numel()
-    _want_all(where, dev, (("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks),
-                           ("lse", lse, torch.float32, (H, total_q)), ("cu_seqlens_q", cu_seqlens_q, torch.int32, (n,)),
-                           ("cu_seqlens_k", cu_seqlens_k, torch.int32, (n,)),
-                           *[(name, t, bf16, qs) for name, t in q_like], *[(name, t, bf16, ks) for name, t in k_like]))
+    if (q.dtype is not bf16 or not q.is_contiguous()
+            or k.dtype is not bf16 or not k.is_contiguous() or k.get_device() != dev
+            or v.dtype is not bf16 or v.shape != ks or not v.is_contiguous() or v.get_device() != dev
+            or o.dtype is not bf16 or o.shape != qs or not o.is_contiguous() or o.get_device() != dev
+            or lse.dtype is not torch.float32 or lse.shape != (H, total_q) or not lse.is_contiguous()
+            or lse.get_device() != dev
+            or cu_seqlens_q.dtype is not i32 or cu_seqlens_q.dim() != 1 or not cu_seqlens_q.is_contiguous()
+            or cu_seqlens_q.get_device() != dev
+            or cu_seqlens_k.dtype is not i32 or cu_seqlens_k.shape != (n,) or not cu_seqlens_k.is_contiguous()
+            or cu_seqlens_k.get_device() != dev):
+        _refuse(where, dev, (("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks), ("o", o, bf16, qs),
+                             ("lse", lse, torch.float32, (H, total_q)), ("cu_seqlens_q", cu_seqlens_q, i32, (n,)),
+                             ("cu_seqlens_k", cu_seqlens_k, i32, (n,))))
     return dev, (n - 1, H, ks[1], d, total_q, ks[0])
 
 
@@ -324,9 +334,14 @@ def fa_fwd_varlen_gqa(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q:
                       scale: float, causal: bool, stream=None) -> None:
     """Packed forward with grouped heads (q [total_q, H, d], k and v
     [total_k, H_kv, d]); same semantics as the C entry point."""
-    dev, sizes = _check_gqa("fa_fwd_varlen_gqa", q, k, v, (("o", o),), (), lse, cu_seqlens_q, cu_seqlens_k)
-    _call("fa_fwd_varlen_gqa", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes, int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)))
+    where = "fa_fwd_varlen_gqa"
+    dev, sizes = _check_gqa(where, q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
+    st = _on_device(dev, (_LIB or load_library()).fa_fwd_varlen_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    o.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes,
+                    int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)),
+                    _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
 def attention_forward_varlen_gqa(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, causal,
@@ -341,14 +356,22 @@ def attention_forward_varlen_gqa(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen
 
 def _bwd_varlen_gqa(fn, q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                     scale, causal, workspace, stream) -> None:
-    dev, sizes = _check_gqa(fn, q, k, v, (("o", o), ("dO", dO), ("dq", dq)), (("dk", dk), ("dv", dv)), lse,
-                            cu_seqlens_q, cu_seqlens_k)
-    workspace, ws, ws_bytes = _workspace(
-        fn, workspace, lambda: fa_bwd_workspace_size(sizes[0], sizes[1], int(max_seqlen_q), sizes[3]), dev,
-        stream)
-    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
-          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes,
-          int(max_seqlen_q), int(max_seqlen_k), float(scale), int(bool(causal)), ws, ws_bytes)
+    dev, sizes = _check_gqa(fn, q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
+    qs, ks, bf16 = q.shape, k.shape, _torch.bfloat16
+    if (dO.dtype is not bf16 or dO.shape != qs or not dO.is_contiguous() or dO.get_device() != dev
+            or dq.dtype is not bf16 or dq.shape != qs or not dq.is_contiguous() or dq.get_device() != dev
+            or dk.dtype is not bf16 or dk.shape != ks or not dk.is_contiguous() or dk.get_device() != dev
+            or dv.dtype is not bf16 or dv.shape != ks or not dv.is_contiguous() or dv.get_device() != dev):
+        _refuse(fn, dev, (("dO", dO, bf16, qs), ("dq", dq, bf16, qs), ("dk", dk, bf16, ks), ("dv", dv, bf16, ks)))
+    workspace = _workspace(fn, workspace, dev, stream, fa_bwd_workspace_size, sizes[0], sizes[1], int(max_seqlen_q),
+                           sizes[3])
+    st = _on_device(dev, getattr(_LIB or load_library(), fn), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                    lse.data_ptr(), dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                    cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *sizes, int(max_seqlen_q), int(max_seqlen_k),
+                    float(scale), int(bool(causal)), workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size(), _raw_stream(fn, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, fn)
 
 
 def fa_bwd_varlen_gqa(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
@@ -518,7 +541,7 @@ def fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_le
                             workspace=None, stream=None) -> None:
     """One decoding step of sequences that share prefixes, over a paged KV
     cache with grouped heads; same semantics as the C entry point."""
-    torch = _load_torch()
+    torch = _torch or _load_torch()
     where = "fa_decode_shared_prefix"
     dev = _cuda_index(where, q)
     qs, cs, bf16, i32 = q.shape, k_cache.shape, torch.bfloat16, torch.int32
@@ -527,19 +550,38 @@ def fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_le
                          f"[rows, blocks per row]; got {tuple(qs)} and {tuple(cs)}")
     B, H, d = qs
     P, prefix_width = prefix_table.shape
-    width = block_table.shape[1]
-    _want_all(where, dev, (
-        ("q", q, bf16, qs), ("k_cache", k_cache, bf16, cs), ("v_cache", v_cache, bf16, cs), ("o", o, bf16, qs),
-        ("lse", lse, torch.float32, (B, H)), ("prefix_table", prefix_table, i32, (P, prefix_width)),
-        ("prefix_lens", prefix_lens, i32, (P,)), ("cu_prefix_seqs", cu_prefix_seqs, i32, (P + 1,)),
-        ("block_table", block_table, i32, (B, width)), ("seq_lens", seq_lens, i32, (B,))))
+    rows, width = block_table.shape
+    if (q.dtype is not bf16 or not q.is_contiguous() or rows != B
+            or k_cache.dtype is not bf16 or not k_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.dtype is not bf16 or v_cache.shape != cs or not v_cache.is_contiguous()
+            or v_cache.get_device() != dev
+            or o.dtype is not bf16 or o.shape != qs or not o.is_contiguous() or o.get_device() != dev
+            or lse.dtype is not torch.float32 or lse.shape != (B, H) or not lse.is_contiguous()
+            or lse.get_device() != dev
+            or prefix_table.dtype is not i32 or not prefix_table.is_contiguous() or prefix_table.get_device() != dev
+            or prefix_lens.dtype is not i32 or prefix_lens.shape != (P,) or not prefix_lens.is_contiguous()
+            or prefix_lens.get_device() != dev
+            or cu_prefix_seqs.dtype is not i32 or cu_prefix_seqs.shape != (P + 1,)
+            or not cu_prefix_seqs.is_contiguous() or cu_prefix_seqs.get_device() != dev
+            or block_table.dtype is not i32 or not block_table.is_contiguous() or block_table.get_device() != dev
+            or seq_lens.dtype is not i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous()
+            or seq_lens.get_device() != dev):
+        _refuse(where, dev, (
+            ("q", q, bf16, qs), ("k_cache", k_cache, bf16, cs), ("v_cache", v_cache, bf16, cs), ("o", o, bf16, qs),
+            ("lse", lse, torch.float32, (B, H)), ("prefix_table", prefix_table, i32, (P, prefix_width)),
+            ("prefix_lens", prefix_lens, i32, (P,)), ("cu_prefix_seqs", cu_prefix_seqs, i32, (P + 1,)),
+            ("block_table", block_table, i32, (B, width)), ("seq_lens", seq_lens, i32, (B,))))
     max_group, max_prefix_len, max_seq_len = int(max_group), int(max_prefix_len), int(max_seq_len)
-    workspace, ws, ws_bytes = _workspace(where, workspace, lambda: fa_decode_shared_prefix_workspace_size(
-        P, B, H, cs[2], d, max_group, max_prefix_len, max_seq_len), dev, stream)
-    _call(where, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          prefix_table.data_ptr(), prefix_lens.data_ptr(), cu_prefix_seqs.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), P, B, H, cs[2], d, cs[0], cs[1], prefix_width, width, max_group, max_prefix_len,
-          max_seq_len, float(scale), ws, ws_bytes)
+    workspace = _workspace(where, workspace, dev, stream, fa_decode_shared_prefix_workspace_size, P, B, H, cs[2], d,
+                           max_group, max_prefix_len, max_seq_len)
+    st = _on_device(dev, (_LIB or load_library()).fa_decode_shared_prefix, q.data_ptr(), k_cache.data_ptr(),
+                    v_cache.data_ptr(), o.data_ptr(), lse.data_ptr(), prefix_table.data_ptr(),
+                    prefix_lens.data_ptr(), cu_prefix_seqs.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                    P, B, H, cs[2], d, cs[0], cs[1], prefix_width, width, max_group, max_prefix_len, max_seq_len,
+                    float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                    _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
 def attention_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
@@ -564,21 +606,33 @@ def _heads_stride(where, name, t, T, H, d, dev) -> int:
 
 
 def _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, of=""):
-    """(device, token strides of q and k, the C call's sizes)."""
-    torch = _load_torch()
+    """Checks what both directions take (q_out, k_out: the outputs, or, of =
+    "d", their gradients): (device, the C call's sizes, token strides of q and k)."""
+    torch = _torch or _load_torch()
     dev = _cuda_index(where, q)
     qs, ks, table = q.shape, k.shape, cos.shape
     if len(qs) != 3 or len(ks) != 3 or len(table) != 2:
         raise ValueError(f"{where}: q is [T, H, d], k [T, H_kv, d], cos and sin [max_pos, rot / 2]; got {tuple(qs)}, "
                          f"{tuple(ks)} and {tuple(table)}")
     T, H, d = qs
-    strides = _heads_stride(where, "q", q, T, H, d, dev), _heads_stride(where, "k", k, T, ks[1], d, dev)
-    bf16, f32 = torch.bfloat16, torch.float32
-    _want_all(where, dev, (("q_weight", q_weight, bf16, (d,)), ("k_weight", k_weight, bf16, (d,)),
-                           ("cos", cos, f32, table), ("sin", sin, f32, table),
-                           ("positions", positions, torch.int32, (T,)), (of + "q_out", q_out, bf16, qs),
-                           (of + "k_out", k_out, bf16, ks)))
-    return dev, strides, (T, H, ks[1], d, 2 * table[1], table[0])
+    H_kv = ks[1]
+    sq, sk = _heads_stride(where, "q", q, T, H, d, dev), _heads_stride(where, "k", k, T, H_kv, d, dev)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if (q_weight.dtype is not bf16 or q_weight.shape != (d,) or not q_weight.is_contiguous()
+            or q_weight.get_device() != dev
+            or k_weight.dtype is not bf16 or k_weight.shape != (d,) or not k_weight.is_contiguous()
+            or k_weight.get_device() != dev
+            or cos.dtype is not f32 or not cos.is_contiguous() or cos.get_device() != dev
+            or sin.dtype is not f32 or sin.shape != table or not sin.is_contiguous() or sin.get_device() != dev
+            or positions.dtype is not i32 or positions.shape != (T,) or not positions.is_contiguous()
+            or positions.get_device() != dev
+            or q_out.dtype is not bf16 or q_out.shape != qs or not q_out.is_contiguous() or q_out.get_device() != dev
+            or k_out.dtype is not bf16 or k_out.shape != ks or not k_out.is_contiguous()
+            or k_out.get_device() != dev):
+        _refuse(where, dev, (("q_weight", q_weight, bf16, (d,)), ("k_weight", k_weight, bf16, (d,)),
+                             ("cos", cos, f32, table), ("sin", sin, f32, table), ("positions", positions, i32, (T,)),
+                             (of + "q_out", q_out, bf16, qs), (of + "k_out", k_out, bf16, ks)))
+    return dev, (T, H, H_kv, d, 2 * table[1], table[0], sq, sk)
 
 
 def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps: float = 1e-6,
@@ -587,10 +641,12 @@ def fa_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out,
     entry point. q and k may be strided over tokens (parts of a fused
     projection); the rotated width is 2 * cos.shape[1]."""
     where = "fa_qk_norm_rope"
-    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
-    _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
-          sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *sizes, *strides, float(eps),
-          int(bool(interleaved)))
+    dev, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
+    st = _on_device(dev, (_LIB or load_library()).fa_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+                    k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(),
+                    k_out.data_ptr(), *sizes, float(eps), int(bool(interleaved)), _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps: float = 1e-6, interleaved: bool = False,
@@ -611,17 +667,23 @@ def fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, d
     """Backward of fa_qk_norm_rope; same semantics as the C entry point. dq
     and dk may be strided over tokens, like q and k."""
     where = "fa_qk_norm_rope_bwd"
-    dev, strides, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, "d")
+    dev, sizes = _check_norm_rope(where, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, "d")
     T, H, H_kv, d = sizes[:4]
-    out_strides = _heads_stride(where, "dq", dq, T, H, d, dev), _heads_stride(where, "dk", dk, T, H_kv, d, dev)
-    _want_all(where, dev, (("dq_weight", dq_weight, _torch.float32, (d,)),
-                           ("dk_weight", dk_weight, _torch.float32, (d,))))
-    workspace, ws, ws_bytes = _workspace(where, workspace,
-                                         lambda: fa_qk_norm_rope_bwd_workspace_size(T, H, H_kv, d), dev, stream)
-    _call(where, dev, stream, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(),
-          sin.data_ptr(), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-          dq_weight.data_ptr(), dk_weight.data_ptr(), *sizes, *strides, *out_strides, float(eps),
-          int(bool(interleaved)), ws, ws_bytes)
+    f32 = _torch.float32
+    sq, sk = _heads_stride(where, "dq", dq, T, H, d, dev), _heads_stride(where, "dk", dk, T, H_kv, d, dev)
+    if (dq_weight.dtype is not f32 or dq_weight.shape != (d,) or not dq_weight.is_contiguous()
+            or dq_weight.get_device() != dev
+            or dk_weight.dtype is not f32 or dk_weight.shape != (d,) or not dk_weight.is_contiguous()
+            or dk_weight.get_device() != dev):
+        _refuse(where, dev, (("dq_weight", dq_weight, f32, (d,)), ("dk_weight", dk_weight, f32, (d,))))
+    workspace = _workspace(where, workspace, dev, stream, fa_qk_norm_rope_bwd_workspace_size, T, H, H_kv, d)
+    st = _on_device(dev, (_LIB or load_library()).fa_qk_norm_rope_bwd, q.data_ptr(), k.data_ptr(),
+                    q_weight.data_ptr(), k_weight.data_ptr(), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(),
+                    dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(),
+                    dk_weight.data_ptr(), *sizes, sq, sk, float(eps), int(bool(interleaved)), workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size(), _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
