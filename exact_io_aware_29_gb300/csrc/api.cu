@@ -277,11 +277,14 @@ void shared_plan(fa::SharedArgs* a) {
   // and 24.5 with 608 prefix items; own parts in 1024 items 1.4 us slower.
   split_keys(static_cast<long long>(a->B) * a->Hk * a->seq_blocks, a->max_seq_len, 608, &a->seq_chunk,
              &a->seq_splits);
-  a->prefix_tiles = group_rows > 32;
+  // More than one 16-row block of the streaming kernel: 128-row tiles. Measured
+  // on prefixes of 2000 / 8000 / 32000 tokens, 8 key heads, d = 128: 24 rows
+  // 15.4 / 18.6 / 37.3 us in tiles, 14.0 / 21.6 / 50.9 streamed; 16 rows 15.3 /
+  // 17.7 / 35.7 in tiles, 12.3 / 15.8 / 33.0 streamed; 64 rows 18.1 / 22.5 /
+  // 40.9 in tiles, 20.8 / 34.5 / 87.7 streamed.
+  a->prefix_tiles = group_rows > 16;
   if (!a->prefix_tiles) {
-    a->prefix_blocks = static_cast<int>((group_rows + 63) / 64);
-    split_keys(static_cast<long long>(a->P) * a->Hk * a->prefix_blocks, a->max_prefix_len, 152, &a->prefix_chunk,
-               &a->prefix_splits);
+    split_keys(static_cast<long long>(a->P) * a->Hk, a->max_prefix_len, 152, &a->prefix_chunk, &a->prefix_splits);
     return;
   }
   // 128-row tiles, two per CTA and one CTA per SM: the number of splits whose

@@ -116,9 +116,10 @@ struct SharedArgs {
   const int* seq_lens;      // int32 [B], clamped to [0, max_seq_len]
   int P, B, H, Hk, D;
   int block_size, num_blocks, max_prefix_blocks, max_blocks, max_group, max_prefix_len, max_seq_len;
-  // The plan (api.cu): key ranges of `chunk` keys, `splits` of them per row,
-  // and row blocks of 64, of the prefix part and of the sequences' own part.
-  int prefix_chunk, prefix_splits, prefix_blocks, seq_chunk, seq_splits, seq_blocks;
+  // The plan (api.cu): key ranges of `chunk` keys, `splits` of them per row, of
+  // the prefix part and of the sequences' own part, whose heads of a key head
+  // go in seq_blocks blocks of 64 rows.
+  int prefix_chunk, prefix_splits, seq_chunk, seq_splits, seq_blocks;
   int prefix_tiles;         // 1: the prefix part runs in 128-row tensor-core tiles (decode_prefix.cu)
   float scale_log2;         // scale * log2(e)
   float* part_o;            // workspace fp32 [B*H, prefix_splits + seq_splits, D], normalised

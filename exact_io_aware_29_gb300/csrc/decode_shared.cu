@@ -7,14 +7,16 @@
 // prefix is computed once per key head for all rows that share it (rows =
 // sequences x G heads of the group), each own part once per sequence.
 //
-// A work item is (rows, key head, key range): up to 64 rows (sequence, head)
-// of one prefix, or the G heads of one sequence on its own tokens. Reading K
-// and V is the bound (4 d bytes per key against 4 d flops per key and row), so
-// one warp streams 64-key tiles through a ring with TMA (a page is a multiple
-// of 64 tokens: no tile crosses one) while four warps compute on 16-row
-// blocks with mma.sync: at up to 16 rows the padded products need about a
-// quarter of that unit's rate at HBM speed. With more than one 16-row block
-// the warps share the blocks out and each takes more keys of the tile.
+// A prefix with more than 16 rows is a dense product (decode_prefix.cu). The
+// rest is streamed here: a work item is (rows, key head, key range), the up to
+// 16 rows (sequence, head) of one prefix or up to 64 heads of one sequence on
+// its own tokens. Reading K and V is the bound (4 d bytes per key against 4 d
+// flops per key and row), so one warp streams 64-key tiles through a ring with
+// TMA (a page is a multiple of 64 tokens: no tile crosses one) while four warps
+// compute on 16-row blocks with mma.sync: at up to 16 rows the padded products
+// need about a quarter of that unit's rate at HBM speed (64 sequences of 4096
+// own tokens, 32/8 heads, d 128: 165 us, 6.5 TB/s). With more than one 16-row
+// block the warps share the blocks out and each takes more keys of the tile.
 //   S = Q K^T (bf16, fp32 sums), p = 2^(scale log2e S - m), O += p V with p
 //   as the sum of two bf16 numbers (hi = bf16(p), lo = bf16(p - hi): relative
 //   error 2^-17), so P costs no more accuracy than the fp32 sums around it.
@@ -93,12 +95,10 @@ template <int D>
 __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedItem& it) {
   using C = SharedCfg<D>;
   const int G = a.H / a.Hk;
-  const int n_prefix_items = a.prefix_tiles ? 0 : a.P * a.Hk * a.prefix_blocks * a.prefix_splits;
+  const int n_prefix_items = a.prefix_tiles ? 0 : a.P * a.Hk * a.prefix_splits;
   if (id < n_prefix_items) {
     const int split = id % a.prefix_splits;
     int x = id / a.prefix_splits;
-    const int blk = x % a.prefix_blocks;
-    x /= a.prefix_blocks;
     it.kvh = x % a.Hk;
     const int p = x / a.Hk;
     int n;
@@ -107,8 +107,8 @@ __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedI
     it.phys = it.table[it.c0 / a.block_size];  // c0 < max_prefix_len: inside the row
     const int L = min(max(a.prefix_lens[p], 0), a.max_prefix_len);
     prefix_seqs(a, p, it.seq0, n);
-    it.row0 = blk * C::ROWS;
-    it.rows = min(n * G - it.row0, C::ROWS);
+    it.row0 = 0;
+    it.rows = min(n * G, 16);  // max_group * G <= 16 here
     it.c1 = min(L, it.c0 + a.prefix_chunk);
     it.slot = split;
   } else {
@@ -432,7 +432,7 @@ static cudaError_t launch_shared_t(const CUtensorMap& tk, const CUtensorMap& tv,
   auto kern = fa_decode_shared_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long items = (a.prefix_tiles ? 0 : static_cast<long long>(a.P) * a.Hk * a.prefix_blocks * a.prefix_splits) +
+  const long long items = (a.prefix_tiles ? 0 : static_cast<long long>(a.P) * a.Hk * a.prefix_splits) +
                           static_cast<long long>(a.B) * a.Hk * a.seq_blocks * a.seq_splits;
   const long long rows = static_cast<long long>(a.B) * a.H;
   if (items > 0x7fffffffLL || rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -183,7 +183,7 @@ def steps():
         "forward big": lambda: binding.fa_fwd_varlen_gqa(qb, kb, vb, ob, lb, big, big, 100, 100, 0.1, True),
         "backward big": lambda: binding.fa_bwd_varlen_gqa(qb, kb, vb, ob, lb, qb, *gb, big, big, 100, 100, 0.1, True, wb),
     }
-    for name, n in (("few", 3), ("many", 40)):  # up to 32 rows, and the tensor-core tiles
+    for name, n in (("few", 3), ("many", 40)):  # streamed, and in tensor-core tiles
         dec = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in
                ([[0, 1, 2, 3]], [250], [0, n], [[4 + i] for i in range(n)], [1 + i % 60 for i in range(n)])]
         kp, vp, qd = rnd(4 + n, PAGE, HK, D), rnd(4 + n, PAGE, HK, D), rnd(n, H, D)
