@@ -958,7 +958,9 @@ int fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_ca
     const fa::QTile qt = q_tile(H / H_kv);
     CUtensorMap tq;
     if (!encode_thd_group(&tq, q, H, B, d, qt)) return launch_error(cudaErrorInvalidValue);
-    const cudaError_t pe = fa::launch_decode_prefix(tq, tk, tv, a, qt, s);
+    fa::LaunchMarks pm;
+    const bool ptimed = next_marks(&pm, 0, 1);
+    const cudaError_t pe = fa::launch_decode_prefix(tq, tk, tv, a, qt, s, ptimed ? &pm : nullptr);
     if (pe != cudaSuccess) return launch_error(pe);
   }
   cudaError_t e = fa::launch_decode_shared(tk, tv, a, s, timed ? &marks : nullptr);

@@ -205,7 +205,7 @@ struct LaunchMarks {
 // The prefix part of that step in tensor-core tiles: Q [B, H, D] in boxes of
 // the tile, K and V in boxes of 64 tokens.
 cudaError_t launch_decode_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 const SharedArgs& a, QTile qt, cudaStream_t stream);
+                                 const SharedArgs& a, QTile qt, cudaStream_t stream, const LaunchMarks* marks);
 cudaError_t set_decode_prefix_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
 int take_decode_prefix_status();
 cudaError_t launch_decode_shared(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,

@@ -18,7 +18,7 @@ int take_decode_prefix_status() { return take_status_here(); }
 
 template <int D>
 static cudaError_t launch_prefix_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                   const SharedArgs& d, QTile qt, cudaStream_t stream) {
+                                   const SharedArgs& d, QTile qt, cudaStream_t stream, const LaunchMarks* marks) {
   using C = FwdCfg<D>;
   auto kern = fa_fwd_kernel<D, false, kShared>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -34,13 +34,16 @@ static cudaError_t launch_prefix_t(const CUtensorMap& tq, const CUtensorMap& tk,
   const long long blocks = static_cast<long long>(d.prefix_splits) * d.P * (d.H / qt.P) *
                            ((d.max_group + 2 * qt.tok - 1) / (2 * qt.tok));
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  mark(marks, true, 0, stream);
   kern<<<static_cast<unsigned>(blocks), C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, a);
+  mark(marks, false, 0, stream);
   return cudaGetLastError();
 }
 
 cudaError_t launch_decode_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 const SharedArgs& a, QTile qt, cudaStream_t stream) {
-  return a.D == 64 ? launch_prefix_t<64>(tq, tk, tv, a, qt, stream) : launch_prefix_t<128>(tq, tk, tv, a, qt, stream);
+                                 const SharedArgs& a, QTile qt, cudaStream_t stream, const LaunchMarks* m) {
+  return a.D == 64 ? launch_prefix_t<64>(tq, tk, tv, a, qt, stream, m)
+                   : launch_prefix_t<128>(tq, tk, tv, a, qt, stream, m);
 }
 
 }  // namespace fa

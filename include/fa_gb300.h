@@ -380,7 +380,10 @@ const char* fa_last_cuda_error(void);
  * fa_timing_read(kind, &ms, &count) waits for the recorded events and returns
  * the summed elapsed time (ms) and the number of timed launches of one kernel:
  * kind 0 = forward, 1 = backward pre-pass, 2 = backward main kernel,
- * 3 = backward dQ conversion. fa_timing_end() releases the events; calls made
+ * 3 = backward dQ conversion. (The grouped-head forms count as the kernels they
+ * are compiled from; a shared-prefix decoding step records its tensor-core
+ * prefix part as kind 0, its streamed part as 4 and the joining kernel as 5.)
+ * fa_timing_end() releases the events; calls made
  * after n launches of a kind are no longer timed. Returns fa_status.
  */
 int fa_timing_begin(int max_calls);

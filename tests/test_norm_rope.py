@@ -247,6 +247,31 @@ def test_captured_on_its_own_stream():
         assert all(torch.equal(a, b) for a, b in zip(out, w))
 
 
+@pytest.mark.gpu
+def test_tensors_past_2_31_elements():
+    """2.2e9 elements of q: rows at both boundaries and at the end equal the
+    same tokens in a call of their own (a row depends on its token alone)."""
+    import torch
+    T, H, Hk, d = 540_000, 32, 1, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    src = torch.randn(1009, (H + Hk) * d, device="cuda", generator=g).to(torch.bfloat16)
+    qkv = src[torch.arange(T, device="cuda") % 1009]
+    q, k = qkv[:, :H * d].view(T, H, d), qkv[:, H * d:].view(T, Hk, d)
+    c = Case(3, 1, 1, d, 128, 9700)
+    pos = (torch.arange(T, device="cuda") % 700).to(torch.int32)
+    args = (*c.w, c.cos, c.sin)
+    yq, yk = binding.qk_norm_rope(q, k, *args, pos)
+    dq, dk, _, _ = binding.qk_norm_rope_backward(q, k, *args, pos, yq, yk)
+    for t0 in (0, 2 ** 30 // (H * d) - 50, 2 ** 31 // (H * d) - 50, 2 ** 31 // ((H + Hk) * d) - 50, T - 100):
+        rows = slice(t0, t0 + 100)
+        y = binding.qk_norm_rope(q[rows], k[rows], *args, pos[rows])
+        x = binding.qk_norm_rope_backward(q[rows], k[rows], *args, pos[rows], *y)
+        torch.cuda.synchronize()
+        for a, b in zip((yq, yk, dq, dk), (*y, *x[:2])):
+            assert torch.equal(a[rows], b)
+
+
 # ------------------------------------------------------------ refusals (host only)
 FAKE = 0x10000
 GOOD = dict(ptr=FAKE, out=FAKE, T=4, H=8, Hk=2, d=64, rot=64, max_pos=10, qs=512, ks=128, eps=1e-6)

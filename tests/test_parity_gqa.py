@@ -62,6 +62,8 @@ CASES = [
     (44, 4, [31, 3], [90, 3]),                             # eleven: one head a tile
     (2, 1, [1000], [1500]),                                # continued prompt over many blocks
     (16, 8, [100 + 9 * i for i in range(20)], [100 + 9 * i for i in range(20)]),  # more key blocks than SMs
+    (64, 1, [5, 130], [40, 130]),                          # 64 heads a tile: two tokens
+    (256, 2, [3, 1, 9], [3, 70, 9]),                       # 128 heads a tile: one token
     (4, 1, [700, 650], [700, 650]),                        # few key blocks: their pairs shared out over CTAs
 ]
 
@@ -244,6 +246,42 @@ def test_captured_and_on_two_streams():
         assert binding.fa_check_status() == binding.FA_OK
         for a, b in zip((*out, *got_other), (*w, *want_other)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_tensors_past_2_31_elements():
+    """A packed batch of 2.2e9 query elements: sequences at its boundaries and at
+    its end give, bit for bit, what they give in a small batch (forward and
+    deterministic backward)."""
+    import torch
+    H, Hk, d, L, B = 32, 4, 128, 1000, 540
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    T = B * L
+    make = lambda h: torch.randn(L, h, d, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    src = {n: [make(h) for _ in range(3)] for n, h in (("q", H), ("k", Hk), ("v", Hk), ("do", H))}
+    full = {n: torch.cat([s[b % 3] for b in range(B)]) for n, s in src.items()}
+    assert full["q"].numel() > 2 ** 31
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * L
+    args = (cu, cu, L, L, d ** -0.5, True)
+    o, lse = binding.attention_forward_varlen_gqa(full["q"], full["k"], full["v"], *args)
+    grads = binding.attention_backward_varlen_gqa(full["q"], full["k"], full["v"], o, lse, full["do"], *args,
+                                                  deterministic=True)
+    # The same sequences in a batch of twenty: as many key blocks per head as
+    # keep it from sharing them out over clusters (which add up in another order).
+    n = 20
+    few = {x: torch.cat([t[b % 3] for b in range(n)]) for x, t in src.items()}
+    cf = cu[:n + 1].contiguous()
+    af = (cf, cf, L, L, d ** -0.5, True)
+    fo, fl = binding.attention_forward_varlen_gqa(few["q"], few["k"], few["v"], *af)
+    fg = binding.attention_backward_varlen_gqa(few["q"], few["k"], few["v"], fo, fl, few["do"], *af,
+                                               deterministic=True)
+    torch.cuda.synchronize()
+    for b in (B - 1, B - 2, 2 ** 30 // (L * H * d), 2 ** 31 // (L * H * d), 0):
+        rows, same = slice(b * L, (b + 1) * L), slice(b % 3 * L, (b % 3 + 1) * L)
+        assert torch.equal(o[rows], fo[same]) and torch.equal(lse[:, rows], fl[:, same])
+        for t, r in zip(grads, fg):
+            assert torch.equal(t[rows], r[same])
 
 
 FAKE = 0x10000  # a 16-byte aligned non-null address; never dereferenced (rejected first)
