@@ -44,6 +44,7 @@
 #pragma once
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -756,46 +757,62 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         // P^T = 2^(S^T * sl2 + nlse2) for 64 queries, 32 at a time; P stays in
-        // registers (bf16 pairs) for dS and goes to TMEM for the dV product.
+        // registers (bf16 pairs; grouped layout: f16) for dS and goes to TMEM as
+        // bf16 for the dV product.
         uint32_t pk[2][16];
+        auto p_phase = [&](auto with_mask) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[32];
-          uint32_t pb16[LAYOUT == kGrouped ? 8 : 16];  // P for dV
-          tmem_ld32(tr + h * 64 + c * 32, s);
-          tmem_wait_ld();
-          const uint64_t sl2x2 = f2_pack(sl2, sl2);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32];
+            uint32_t pb16[LAYOUT == kGrouped ? 8 : 16];  // P for dV
+            tmem_ld32(tr + h * 64 + c * 32, s);
+            tmem_wait_ld();
+            const uint64_t sl2x2 = f2_pack(sl2, sl2);
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse2v + c * 32 + q4 * 4);  // -LSE*log2(e)
-            const uint64_t lp[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(lse2v + c * 32 + q4 * 4);  // -LSE*log2(e)
+              const uint64_t lp[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int q = q4 * 2 + e;
-              const int qa = h * 64 + c * 32 + 2 * q;  // query column within the block
-              float xa, xb;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), sl2x2, lp[e]), xa, xb);
-              float pa = ex2(xa);
-              float pb = ex2(xb);
-              if (!kvalid) pa = pb = 0.f;
-              if (diag) {
-                if (qa < lim) pa = 0.f;
-                if (qa + 1 < lim) pb = 0.f;
+              for (int e = 0; e < 2; ++e) {
+                const int q = q4 * 2 + e;
+                const int qa = h * 64 + c * 32 + 2 * q;  // query column within the block
+                float xa, xb;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), sl2x2, lp[e]), xa, xb);
+                float pa = ex2(xa);
+                float pb = ex2(xb);
+                if constexpr (decltype(with_mask)::value) {
+                  if (!kvalid) pa = pb = 0.f;
+                  if (diag) {
+                    if (qa < lim) pa = 0.f;
+                    if (qa + 1 < lim) pb = 0.f;
+                  }
+                }
+                if constexpr (LAYOUT == kGrouped) {
+                  pb16[q & 7] = pack_bf16x2(pa, pb);
+                  pk[c][q] = pack_f16x2(pa, pb);  // P for dS
+                } else {
+                  pk[c][q] = pb16[q] = pack_bf16x2(pa, pb);
+                }
               }
+              // Columns already read; halves of 8 keep fewer registers alive.
               if constexpr (LAYOUT == kGrouped) {
-                pb16[q & 7] = pack_bf16x2(pa, pb);
-                pk[c][q] = pack_f16x2(pa, pb);  // P for dS
-              } else {
-                pk[c][q] = pb16[q] = pack_bf16x2(pa, pb);
+                if ((q4 & 3) == 3) tmem_st8(tr + h * 64 + c * 16 + (q4 >> 2) * 8, pb16);
               }
             }
-            // Columns already read; halves of 8 keep fewer registers alive.
-            if constexpr (LAYOUT == kGrouped) {
-              if ((q4 & 3) == 3) tmem_st8(tr + h * 64 + c * 16 + (q4 >> 2) * 8, pb16);
-            }
+            if constexpr (LAYOUT != kGrouped) tmem_st16(tr + h * 64 + c * 16, pb16);
           }
-          if constexpr (LAYOUT != kGrouped) tmem_st16(tr + h * 64 + c * 16, pb16);
-        }
+        };
+        // Grouped layout: most pairs have no masked entry (every key is the
+        // sequence's and seen by every query of the block); they take a copy of
+        // the code without the masks (8 sequences of up to 4096 tokens, 16/4
+        // heads, d 128, forward + backward: 1572 -> 1419 us). The compiler does
+        // the same for the fixed layout's diagonal by itself.
+        const bool masked = LAYOUT != kGrouped || wk.key0 + C::BN > wk.sv.Lk ||
+                            (CAUSAL && wk.key0 + C::BN - 1 - wk.sv.shift - qb * C::BM > 0);
+        if (masked)
+          p_phase(std::true_type{});
+        else
+          p_phase(std::false_type{});
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_ready);
