@@ -510,7 +510,7 @@ int fa_fwd_varlen_gqa(const void* q, const void* k, const void* v, void* o, floa
   if (st != FA_OK) return st;
   st = apply_test_hooks(s);
   if (st != FA_OK) return st;
-  fa::FwdArgs a;
+  fa::FwdGroupedArgs a;
   a.qt = q_tile(H / H_kv);
   CUtensorMap tq, tk, tv;
   if (!encode_thd_group(&tq, q, H, total_q, d, a.qt) || !encode_thd(&tk, k, H_kv, total_k, d, 128) ||

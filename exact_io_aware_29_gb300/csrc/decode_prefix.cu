@@ -23,7 +23,7 @@ static cudaError_t launch_prefix_t(const CUtensorMap& tq, const CUtensorMap& tk,
   auto kern = fa_fwd_kernel<D, false, kShared>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  FwdArgs a{};
+  FwdSharedArgs a{};
   a.dec = d;
   a.qt = qt;
   a.s.B = d.B;

@@ -19,8 +19,8 @@ cudaError_t set_fwd_gqa_test_hooks(unsigned long long wait_limit_ns, int drop_lo
 
 int take_fwd_gqa_status() { return take_status_here(); }
 
-cudaError_t launch_fwd_gqa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdArgs& a,
-                           cudaStream_t stream, const LaunchMarks* m) {
+cudaError_t launch_fwd_gqa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const FwdGroupedArgs& a, cudaStream_t stream, const LaunchMarks* m) {
   const bool c = a.s.causal != 0;
   if (a.s.D == 64)
     return c ? launch_fwd_t<64, true, kGrouped>(tq, tk, tv, a, stream, m)

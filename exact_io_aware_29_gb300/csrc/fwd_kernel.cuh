@@ -293,25 +293,39 @@ struct FwdShared {
 // What one CTA works on: two 128-row Q tiles of one (b, h), or, grouped, of P
 // heads of one key head's group (tok tokens each).
 struct FwdCta {
+  static constexpr int tok = 128;  // query tokens per tile
   int q0, bh, hh, klim, n_max;
-  int kvh;     // key head
-  int tok;     // query tokens per tile (the tile's rows, over P heads when grouped)
-  int key0, slot;    // shared-prefix layout: the CTA's first key of the prefix, its partial's index,
-  const int* table;  // and the prefix's pages
   int own;     // bit t: this CTA computes and writes tile t (both, unless the pair is split)
   int n_t[2];  // key blocks each Q tile visits (fully masked blocks are skipped)
   SeqView sv;
   uint32_t tmem;
+  __device__ __forceinline__ int key_head() const { return hh; }
 };
+struct FwdGroupedCta : FwdCta {
+  int tok, kvh;  // the tile's rows are tok tokens of P heads from hh on, all of key head kvh
+  __device__ __forceinline__ int key_head() const { return kvh; }
+};
+struct FwdSharedCta : FwdGroupedCta {
+  int key0, slot;    // the CTA's first key of the prefix, its partial's index
+  const int* table;  // the prefix's pages
+};
+template <int LAYOUT>
+struct FwdCtaOf { using type = FwdCta; };
+template <>
+struct FwdCtaOf<kGrouped> { using type = FwdGroupedCta; };
+template <>
+struct FwdCtaOf<kShared> { using type = FwdSharedCta; };
+template <int LAYOUT>
+using FwdCtaT = typename FwdCtaOf<LAYOUT>::type;
 
 // Shared-prefix layout: CTAs that read the same keys (the row tiles and heads
 // of one key range) are neighbours in the grid.
 template <int D>
-__device__ __forceinline__ FwdCta fwd_cta_shared(const FwdArgs& args) {
+__device__ __forceinline__ FwdSharedCta fwd_cta_shared(const FwdSharedArgs& args) {
   using C = FwdCfg<D>;
   const SharedArgs& a = args.dec;
   const int cols = a.H / args.qt.P, n_pairs = (a.max_group + 2 * args.qt.tok - 1) / (2 * args.qt.tok);
-  FwdCta c;
+  FwdSharedCta c;
   c.tok = args.qt.tok;
   int x = blockIdx.x;
   const int pair = x % n_pairs;
@@ -338,59 +352,61 @@ __device__ __forceinline__ FwdCta fwd_cta_shared(const FwdArgs& args) {
 }
 
 template <int D, bool CAUSAL, int LAYOUT>
-__device__ __forceinline__ FwdCta fwd_cta(const FwdArgs& args) {
-  if constexpr (LAYOUT == kShared) return fwd_cta_shared<D>(args);
-  using C = FwdCfg<D>;
-  const AttnShape& sh = args.s;
-  FwdCta c;
-  c.tok = tile_of_heads(LAYOUT) ? args.qt.tok : C::BM;
-  const int heads = tile_of_heads(LAYOUT) ? sh.H / args.qt.P : sh.H;  // Q tile columns per sequence
-  const int BH = sh.B * heads;
-  const int n_pairs = (sh.N + 2 * c.tok - 1) / (2 * c.tok);
-  // The grid runs in groups of heads whose K and V fit the L2 together (every
-  // Q pair of a head reads all of its K and V), and inside a group heaviest
-  // causal tiles first: the last Q pair of every head of the group leads.
-  // The last pairs of the grid order may run as two single-tile CTAs (the
-  // launch adds one CTA per split pair): pairs [2 P - grid, P).
-  const int P = BH * n_pairs;
-  const int split_from = 2 * P - static_cast<int>(gridDim.x);
-  int lin = blockIdx.x;
-  int own = 3;
-  if (lin >= split_from) {
-    const int sidx = lin - split_from;
-    lin = split_from + (sidx >> 1);
-    own = 1 << (sidx & 1);
-  }
-  const int G = min(BH, max(1, args.heads_per_group));
-  const int group = lin / (G * n_pairs);
-  const int gsize = min(G, BH - group * G);
-  const int r_in = lin - group * G * n_pairs;
-  const int pair = n_pairs - 1 - r_in / gsize;
-  c.bh = group * G + r_in % gsize;
-  c.hh = c.bh % heads;
-  c.kvh = c.hh;
-  if (tile_of_heads(LAYOUT)) {
-    c.hh *= args.qt.P;  // the tile's first head
-    c.kvh = c.hh / (sh.H / sh.Hk);
-  }
-  c.q0 = pair * 2 * c.tok;
-  c.sv = seq_view<LAYOUT>(args.pk, args.kv_lens, c.bh / heads, sh.N, sh.Nk);
-  c.klim = c.sv.Lk;
+__device__ __forceinline__ FwdCtaT<LAYOUT> fwd_cta(const FwdArgsT<LAYOUT>& args) {
+  if constexpr (LAYOUT == kShared) {
+    return fwd_cta_shared<D>(args);
+  } else {
+    using C = FwdCfg<D>;
+    const AttnShape& sh = args.s;
+    FwdCtaT<LAYOUT> c;
+    if constexpr (LAYOUT == kGrouped) c.tok = args.qt.tok;
+    const int heads = sh.H / args.qt.P;  // Q tile columns per sequence
+    const int BH = sh.B * heads;
+    const int n_pairs = (sh.N + 2 * c.tok - 1) / (2 * c.tok);
+    // The grid runs in groups of heads whose K and V fit the L2 together (every
+    // Q pair of a head reads all of its K and V), and inside a group heaviest
+    // causal tiles first: the last Q pair of every head of the group leads.
+    // The last pairs of the grid order may run as two single-tile CTAs (the
+    // launch adds one CTA per split pair): pairs [2 P - grid, P).
+    const int P = BH * n_pairs;
+    const int split_from = 2 * P - static_cast<int>(gridDim.x);
+    int lin = blockIdx.x;
+    int own = 3;
+    if (lin >= split_from) {
+      const int sidx = lin - split_from;
+      lin = split_from + (sidx >> 1);
+      own = 1 << (sidx & 1);
+    }
+    const int G = min(BH, max(1, args.heads_per_group));
+    const int group = lin / (G * n_pairs);
+    const int gsize = min(G, BH - group * G);
+    const int r_in = lin - group * G * n_pairs;
+    const int pair = n_pairs - 1 - r_in / gsize;
+    c.bh = group * G + r_in % gsize;
+    c.hh = c.bh % heads;
+    if constexpr (LAYOUT == kGrouped) {
+      c.hh *= args.qt.P;  // the tile's first head
+      c.kvh = c.hh / (sh.H / sh.Hk);
+    }
+    c.q0 = pair * 2 * c.tok;
+    c.sv = seq_view<LAYOUT>(args.pk, args.kv_lens, c.bh / heads, sh.N, sh.Nk);
+    c.klim = c.sv.Lk;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int rs = c.q0 + t * c.tok;
-    int kmax = c.klim;
-    if (CAUSAL) kmax = min(kmax, rs + c.tok + c.sv.shift);  // last row of the tile sees keys < this
-    c.n_t[t] = (rs >= c.sv.Lq || kmax <= 0 || !((own >> t) & 1)) ? 0 : (kmax + C::BN - 1) / C::BN;
+    for (int t = 0; t < 2; ++t) {
+      const int rs = c.q0 + t * c.tok;
+      int kmax = c.klim;
+      if (CAUSAL) kmax = min(kmax, rs + c.tok + c.sv.shift);  // last row of the tile sees keys < this
+      c.n_t[t] = (rs >= c.sv.Lq || kmax <= 0 || !((own >> t) & 1)) ? 0 : (kmax + C::BN - 1) / C::BN;
+    }
+    c.own = own;
+    c.n_max = max(c.n_t[0], c.n_t[1]);
+    return c;
   }
-  c.own = own;
-  c.n_max = max(c.n_t[0], c.n_t[1]);
-  return c;
 }
 
 // Query row (token) of row rr of a Q tile that starts at row_start.
 template <int LAYOUT>
-__device__ __forceinline__ int fwd_row(const FwdArgs& args, int row_start, int rr) {
+__device__ __forceinline__ int fwd_row(const FwdArgsT<LAYOUT>& args, int row_start, int rr) {
   return row_start + (tile_of_heads(LAYOUT) ? rr / args.qt.P : rr);
 }
 
@@ -399,24 +415,26 @@ __device__ __forceinline__ int fwd_row(const FwdArgs& args, int row_start, int r
 // Returns the ring position after the last load issued (g0 + i1 unless a wait
 // gave up).
 template <int D, int LAYOUT>
-__device__ __forceinline__ int fwd_load_kv_range(const FwdArgs& args, const FwdShared<D>& sm, const FwdCta& c,
-                                                 const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int i0,
-                                                 int i1) {
+__device__ __forceinline__ int fwd_load_kv_range(const FwdArgsT<LAYOUT>& args, const FwdShared<D>& sm,
+                                                 const FwdCtaT<LAYOUT>& c, const CUtensorMap* tmK,
+                                                 const CUtensorMap* tmV, int g0, int i0, int i1) {
   using C = FwdCfg<D>;
   int z2[2] = {0, 0};  // shared-prefix layout: pool rows of the block's two 64-key halves
   for (int idx = i0; idx < i1; ++idx) {
     const int g = g0 + idx;
     const int slot = g % C::STAGES;
     const int use = g / C::STAGES;
-    if (LAYOUT == kShared && (idx == i0 || !(idx & 1))) {
-      // K_j and V_j lie in the same pages. Keys past the range and block ids
-      // outside the pool read as zeros (TMA fills outside the tensor).
-      const SharedArgs& a = args.dec;
+    if constexpr (LAYOUT == kShared) {
+      if (idx == i0 || !(idx & 1)) {
+        // K_j and V_j lie in the same pages. Keys past the range and block ids
+        // outside the pool read as zeros (TMA fills outside the tensor).
+        const SharedArgs& a = args.dec;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rel = (idx >> 1) * C::BN + h * 64, key = c.key0 + rel, page = key / a.block_size;
-        const int phys = rel < c.klim ? c.table[page] : -1;
-        z2[h] = phys < 0 || phys >= a.num_blocks ? -64 : phys * a.block_size + (key - page * a.block_size);
+        for (int h = 0; h < 2; ++h) {
+          const int rel = (idx >> 1) * C::BN + h * 64, key = c.key0 + rel, page = key / a.block_size;
+          const int phys = rel < c.klim ? c.table[page] : -1;
+          z2[h] = phys < 0 || phys >= a.num_blocks ? -64 : phys * a.block_size + (key - page * a.block_size);
+        }
       }
     }
     if (use > 0 && !mbar_wait(&sm.kv_empty[slot], (use - 1) & 1, sm.abort_flag)) return g;
@@ -424,7 +442,7 @@ __device__ __forceinline__ int fwd_load_kv_range(const FwdArgs& args, const FwdS
     const CUtensorMap* tm = (idx & 1) ? tmV : tmK;
     uint8_t* dst = sm.smem + C::OFF_KV + slot * C::KV_BYTES;
     const int row = (idx >> 1) * C::BN;
-    const int y = LAYOUT != kFixed ? c.kvh : row;
+    const int y = LAYOUT != kFixed ? c.key_head() : row;
     const int z = LAYOUT != kFixed ? c.sv.k_start + row : c.bh;
     if constexpr (LAYOUT == kShared) {
 #pragma unroll
@@ -445,8 +463,8 @@ __device__ __forceinline__ int fwd_load_kv_range(const FwdArgs& args, const FwdS
 // ... Returns the ring position after the last load issued (g0 + 2 n unless a
 // wait gave up).
 template <int D, int LAYOUT>
-__device__ __forceinline__ int fwd_load_kv(const FwdArgs& args, const FwdShared<D>& sm, const FwdCta& c,
-                                           const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int n) {
+__device__ __forceinline__ int fwd_load_kv(const FwdArgsT<LAYOUT>& args, const FwdShared<D>& sm,
+                                           const FwdCtaT<LAYOUT>& c, const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int n) {
   return fwd_load_kv_range<D, LAYOUT>(args, sm, c, tmK, tmV, g0, 0, 2 * n);
 }
 
@@ -546,8 +564,8 @@ __device__ __forceinline__ bool fwd_mma_pass(const FwdShared<D>& sm, uint32_t tm
 // blocks: the online-softmax recurrence, P back into TMEM (f16 in the first
 // pass, bf16 in the second), O rescaled lazily. Returns false if a wait gave
 // up; m_used and l are the row's reference max (base 2) and sum of P.
-template <int D, bool CAUSAL, bool BF16>
-__device__ __forceinline__ bool fwd_softmax_pass(const FwdShared<D>& sm, const FwdCta& c, int t, int r, uint32_t tS,
+template <int D, bool CAUSAL, bool BF16, typename Cta>
+__device__ __forceinline__ bool fwd_softmax_pass(const FwdShared<D>& sm, const Cta& c, int t, int r, uint32_t tS,
                                                  uint32_t tO, float sl2, int phase0, float& m_used, float& l) {
   using C = FwdCfg<D>;
   const int nt = c.n_t[t];
@@ -627,7 +645,7 @@ __device__ __forceinline__ bool fwd_softmax_pass(const FwdShared<D>& sm, const F
 // Epilogue of one row: O = acc / l (times ``unscale``) as bf16 and LSE.
 // Returns the row's largest |O| (NaN if an element is NaN).
 template <int D, int LAYOUT>
-__device__ __forceinline__ float fwd_epilogue(const FwdArgs& args, const FwdCta& c, int r, uint32_t tO, bool have_o,
+__device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, const FwdCtaT<LAYOUT>& c, int r, uint32_t tO, bool have_o,
                                               float m_used, float l, float unscale, int rr) {
   const bool valid = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || rr < args.qt.tok * args.qt.P);
   // Flattened query head of the row (grouped: row rr of the tile is head hh + rr % P).
@@ -699,7 +717,7 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgs& args, const FwdCta&
 // + 2 n_r) the pass itself; every barrier continues from its first-pass phase.
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL, int LAYOUT>
-__device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtensorMap* tmV, FwdArgs args, FwdCta c,
+__device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtensorMap* tmV, FwdArgsT<LAYOUT> args, FwdCtaT<LAYOUT> c,
                                            uint32_t mask) {
   using C = FwdCfg<D>;
   const FwdShared<D> sm(reinterpret_cast<uint8_t*>(
@@ -790,13 +808,13 @@ __device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtenso
 template <int D, bool CAUSAL, int LAYOUT>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const FwdArgs args) {
+                  const __grid_constant__ CUtensorMap tmV, const FwdArgsT<LAYOUT> args) {
   using C = FwdCfg<D>;
   const FwdShared<D> sm(reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(fwd_smem_base()) + 1023) & ~uintptr_t(1023)));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  FwdCta c = fwd_cta<D, CAUSAL, LAYOUT>(args);
+  FwdCtaT<LAYOUT> c = fwd_cta<D, CAUSAL, LAYOUT>(args);
   // Packed batches size the grid by the longest sequence: a CTA whose tiles
   // lie past the end of its sequence has nothing to write and leaves before
   // any set-up (the whole CTA takes this branch).
@@ -962,9 +980,9 @@ static long long current_sm_count() {
 
 template <int D, bool CAUSAL, int LAYOUT>
 static cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const FwdArgs& args, cudaStream_t stream, const LaunchMarks* marks) {
+                                const FwdArgsT<LAYOUT>& args, cudaStream_t stream, const LaunchMarks* marks) {
   using C = FwdCfg<D>;
-  FwdArgs a = args;
+  FwdArgsT<LAYOUT> a = args;
   auto kern = fa_fwd_kernel<D, CAUSAL, LAYOUT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
