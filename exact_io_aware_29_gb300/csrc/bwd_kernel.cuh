@@ -250,16 +250,41 @@ __device__ __forceinline__ BwdWork bwd_work(const BwdArgs& args, int item) {
   // key blocks go heaviest first (causal: block j sees nkb - j query blocks)
   // across the group's heads; deterministic order: lightest first, see the
   // dQ reduction issuer.
+  // Grouped layout, causal, default order: an item carries the pairs of all
+  // heads of its group, so that the last group's heavy items, begun late, would
+  // leave most SMs idle at the end. The lightest `late_blocks` key blocks of
+  // every head are therefore kept back until all groups have had their others.
+  // And key blocks count from the end of their own sequence, so that in a
+  // ragged batch too the work goes down from item to item. Forward + backward,
+  // d 128: 8 sequences of 1024..4096 tokens, 16/4 heads 1427 -> 1384 us; 8 of
+  // 2500, 16/2 heads 960 -> 830; 12 of up to 2048, 32/8 heads 608 -> 589; where
+  // there are many items (8 of 8192, 32/8 heads) it changes nothing. All heads
+  // in one group balance as well, but overflow the L2 (8 of 8192: 12.9 -> 17 ms).
   const int heads = LAYOUT == kGrouped ? sh.Hk : sh.H;
   const int BH = sh.B * heads;
-  const int G = min(BH, max(1, args.heads_per_group));
-  const int group = item / (G * nkb);
+  constexpr bool LATE = LAYOUT == kGrouped && CAUSAL && !DET;
+  int G = min(BH, max(1, args.heads_per_group));
+  int first = 0, blocks = nkb;  // key blocks of this part of the order
+  if (LATE) {
+    blocks = nkb - args.late_blocks;
+    if (item >= BH * blocks) {
+      item -= BH * blocks;
+      first = blocks;
+      blocks = args.late_blocks;
+      G = min(BH, max(1, args.late_group));
+    }
+  }
+  const int group = item / (G * blocks);
   const int gsize = min(G, BH - group * G);
-  const int r_in = item - group * G * nkb;
+  const int r_in = item - group * G * blocks;
   BwdWork w;
-  w.j = DET ? nkb - 1 - r_in / gsize : r_in / gsize;
+  w.j = DET ? nkb - 1 - r_in / gsize : first + r_in / gsize;
   w.bh = group * G + r_in % gsize;
   w.sv = seq_view<LAYOUT>(args.pk, args.kv_lens, w.bh / heads, sh.N, sh.Nk);
+  if (LATE) {  // the blocks that a shorter sequence lacks come out past its end
+    w.j -= nkb - (w.sv.Lk + C::BN - 1) / C::BN;
+    if (w.j < 0) w.j += nkb;
+  }
   w.key0 = w.j * C::BN;
   // Query r sees key c iff c <= r + shift (causal): the first query block that
   // sees key block j starts at row key0 - shift.
@@ -1261,6 +1286,15 @@ static cudaError_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, co
     const long long l2 = l2_cache_bytes();
     const long long g = l2 > 0 ? l2 / per_head : 16;
     a.heads_per_group = balanced_heads_per_group(BH / share, g);
+    // The late key blocks (bwd_work): as many as hold a quarter of the
+    // heaviest item's pairs per SM, all heads together, and groups that keep
+    // the query blocks that these items see within the L2.
+    a.late_blocks = 0;
+    if (LAYOUT == kGrouped && CAUSAL && !DET) {
+      while (a.late_blocks < nkb && (a.late_blocks + 1LL) * (a.late_blocks + 1LL) * (BH / share) <= 76LL * nkb)
+        ++a.late_blocks;
+      a.late_group = balanced_heads_per_group(BH / share, std::max(g, 1LL) * nkb / std::max(a.late_blocks, 1));
+    }
   }
   constexpr int TPR = D / 8;
   // The three kernels are launched with programmatic stream serialization:

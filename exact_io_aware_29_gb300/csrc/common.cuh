@@ -172,6 +172,8 @@ struct BwdArgs {
   uint32_t* ticket;    // workspace u32: next work item to hand to a starting CTA
   int deterministic;   // 1: dQ tiles summed in a fixed (descending) key-block order
   int heads_per_group; // set at launch: heads whose work items run together (L2-sized)
+  int late_blocks;     // set at launch (grouped layout): key blocks of each head kept back for the end
+  int late_group;      // set at launch (grouped layout): heads per group there
 };
 
 // FP8 (E4M3) block quantisation of one bf16 tensor (fp8.cu).

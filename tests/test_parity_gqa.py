@@ -188,6 +188,35 @@ def test_rows_of_no_sequence_stay_as_they_were(H, Hk, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk,d,lq,lk", [
+    (8, 2, 128, [6000, 1, 0, 2200, 129, 700, 4100, 128], [6000, 1, 90, 2500, 129, 600, 4100, 0]),
+    (12, 12, 64, [2000, 30, 1500, 900, 1999], [2000, 30, 1500, 900, 1999]),
+    (16, 4, 128, [900 - 40 * i for i in range(20)], [900 - 40 * i for i in range(20)]),
+])
+def test_backward_orders_take_every_key_block_once(H, Hk, d, lq, lk):
+    """The default order starts heavy key blocks first and keeps light ones
+    back, the deterministic one counts them off plainly. Each key block's dK
+    and dV sum over the same pairs in the same order in both, bit for bit; dQ
+    sums over key blocks in another order: two bf16 roundings of nearly equal
+    values, at most 2^-8 of the largest apart. No row stays unwritten."""
+    import torch
+    x = Packed(lq, lk, H, Hk, d, 7700)
+    o, lse = binding.attention_forward_varlen_gqa(*x.qkv(), *x.args(True))
+    out = []
+    for f in (binding.fa_bwd_varlen_gqa, binding.fa_bwd_varlen_gqa_deterministic):
+        g = [torch.full_like(x.dev[n], float("nan")) for n in ("q", "k", "v")]
+        f(*x.qkv(), o, lse, x.dev["do"], *g, *x.args(True))
+        out.append(g)
+    torch.cuda.synchronize()
+    assert binding.fa_check_status() == binding.FA_OK
+    (dq, dk, dv), (rq, rk, rv) = out
+    assert torch.equal(dk.view(torch.int16), rk.view(torch.int16))
+    assert torch.equal(dv.view(torch.int16), rv.view(torch.int16))
+    assert bool(torch.isfinite(dq).all()) and bool(torch.isfinite(dk).all())
+    assert float((dq.float() - rq.float()).abs().max()) <= 1e-2 * float(rq.float().abs().max())
+
+
+@pytest.mark.gpu
 def test_values_outside_f16_take_the_second_pass():
     """A V beyond f16's range makes its tiles run again in bf16, grouped tiles
     (126 of 128 rows in use) among them. O is linear in V: 1e-2 * scale of V."""
