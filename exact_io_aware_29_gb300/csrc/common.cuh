@@ -140,6 +140,7 @@ struct FwdArgs {
 
 struct FwdGroupedArgs : FwdArgs {
   QTile qt;
+  int group_seqs;  // set at launch where only Q pairs that exist have CTAs: sequences per group
 };
 struct FwdSharedArgs : FwdGroupedArgs {
   SharedArgs dec;

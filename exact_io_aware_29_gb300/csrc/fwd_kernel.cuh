@@ -351,7 +351,70 @@ __device__ __forceinline__ FwdSharedCta fwd_cta_shared(const FwdSharedArgs& args
   return c;
 }
 
-template <int D, bool CAUSAL, int LAYOUT>
+// Grouped layout, a batch whose sequences are much shorter than the longest:
+// the grid has a CTA for each Q pair that exists (and up to one per sequence
+// and tile column more, which find nothing), and a CTA finds its own. Order:
+// groups of sequences whose K and V fit the L2, inside a group the highest
+// pair index (the heaviest causal pairs) of all sequences first, inside an
+// index sequence by sequence. Each warp counts the pairs of index >= x, a
+// lane per sequence, and bisects over x. Sets the pair and the flattened tile
+// column; a pair past every sequence where there is none left.
+__device__ __forceinline__ void find_pair(const FwdGroupedArgs& args, int cols, int n_pairs, int& pair, int& bh) {
+  const int lane = threadIdx.x & 31, B = args.s.B, span = 2 * args.qt.tok;
+  auto seq_pairs = [&](int s, int end) {  // 0 past the group
+    if (s >= end) return 0;
+    const int start = min(max(args.pk.cu_q[s], 0), args.pk.total_q);
+    const int L = min(max(args.pk.cu_q[s + 1] - start, 0), min(args.s.N, args.pk.total_q - start));
+    return (L + span - 1) / span;
+  };
+  int k = blockIdx.x;
+  pair = n_pairs;
+  bh = 0;
+  for (int first = 0; first < B; first += args.group_seqs) {
+    const int end = min(B, first + args.group_seqs);
+    const int n0 = seq_pairs(first + lane, end);  // the first 32 stay in registers
+    if (first + lane < end) prefetch_l1(args.pk.cu_k + first + lane);  // read once the CTA's sequence is known
+    auto tiles_from = [&](int x) {  // CTAs of the group's pairs of index >= x
+      int sum = max(0, n0 - x);
+      for (int s = first + 32 + lane; s < end; s += 32) sum += max(0, seq_pairs(s, end) - x);
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(sum))) * cols;
+    };
+    const int all = tiles_from(0);
+    if (k >= all) {
+      k -= all;
+      continue;
+    }
+    int lo = 0, hi = n_pairs, above = 0;  // tiles_from(lo) > k >= tiles_from(hi) = above
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1, m = tiles_from(mid);
+      if (m > k) {
+        lo = mid;
+      } else {
+        hi = mid;
+        above = m;
+      }
+    }
+    k -= above;
+    int i = k / cols;  // the i-th of the group's sequences that has this pair
+    pair = lo;
+    bh = k - i * cols;
+    for (int s0 = first; s0 < end; s0 += 32) {
+      const int n = s0 == first ? n0 : seq_pairs(s0 + lane, end);
+      const unsigned has = __ballot_sync(0xffffffffu, n > lo);
+      if (i < __popc(has)) {
+        const unsigned hit = __ballot_sync(0xffffffffu, n > lo && __popc(has & ((1u << lane) - 1)) == i);
+        bh += (s0 + __ffs(hit) - 1) * cols;
+        break;
+      }
+      i -= __popc(has);
+    }
+    return;
+  }
+}
+
+// FIND: the grid holds only the Q pairs that exist (find_pair); a kernel of its
+// own, since the search merely being in the code cost short prompts 2 %.
+template <int D, bool CAUSAL, int LAYOUT, bool FIND>
 __device__ __forceinline__ FwdCtaT<LAYOUT> fwd_cta(const FwdArgsT<LAYOUT>& args) {
   if constexpr (LAYOUT == kShared) {
     return fwd_cta_shared<D>(args);
@@ -368,21 +431,25 @@ __device__ __forceinline__ FwdCtaT<LAYOUT> fwd_cta(const FwdArgsT<LAYOUT>& args)
     // causal tiles first: the last Q pair of every head of the group leads.
     // The last pairs of the grid order may run as two single-tile CTAs (the
     // launch adds one CTA per split pair): pairs [2 P - grid, P).
-    const int P = BH * n_pairs;
-    const int split_from = 2 * P - static_cast<int>(gridDim.x);
-    int lin = blockIdx.x;
-    int own = 3;
-    if (lin >= split_from) {
-      const int sidx = lin - split_from;
-      lin = split_from + (sidx >> 1);
-      own = 1 << (sidx & 1);
+    int pair, own = 3;
+    if constexpr (FIND) {
+      find_pair(args, heads, n_pairs, pair, c.bh);
+    } else {
+      const int P = BH * n_pairs;
+      const int split_from = 2 * P - static_cast<int>(gridDim.x);
+      int lin = blockIdx.x;
+      if (lin >= split_from) {
+        const int sidx = lin - split_from;
+        lin = split_from + (sidx >> 1);
+        own = 1 << (sidx & 1);
+      }
+      const int G = min(BH, max(1, args.heads_per_group));
+      const int group = lin / (G * n_pairs);
+      const int gsize = min(G, BH - group * G);
+      const int r_in = lin - group * G * n_pairs;
+      pair = n_pairs - 1 - r_in / gsize;
+      c.bh = group * G + r_in % gsize;
     }
-    const int G = min(BH, max(1, args.heads_per_group));
-    const int group = lin / (G * n_pairs);
-    const int gsize = min(G, BH - group * G);
-    const int r_in = lin - group * G * n_pairs;
-    const int pair = n_pairs - 1 - r_in / gsize;
-    c.bh = group * G + r_in % gsize;
     c.hh = c.bh % heads;
     if constexpr (LAYOUT == kGrouped) {
       c.hh *= args.qt.P;  // the tile's first head
@@ -805,7 +872,7 @@ __device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtenso
   }
 }
 
-template <int D, bool CAUSAL, int LAYOUT>
+template <int D, bool CAUSAL, int LAYOUT, bool FIND = false>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const FwdArgsT<LAYOUT> args) {
@@ -814,7 +881,7 @@ __global__ void __launch_bounds__(384, 1)
       (reinterpret_cast<uintptr_t>(fwd_smem_base()) + 1023) & ~uintptr_t(1023)));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  FwdCtaT<LAYOUT> c = fwd_cta<D, CAUSAL, LAYOUT>(args);
+  FwdCtaT<LAYOUT> c = fwd_cta<D, CAUSAL, LAYOUT, FIND>(args);
   // Packed batches size the grid by the longest sequence: a CTA whose tiles
   // lie past the end of its sequence has nothing to write and leaves before
   // any set-up (the whole CTA takes this branch).
@@ -1011,6 +1078,27 @@ static cudaError_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, co
     const long long sms = current_sm_count();
     const long long rem = sms > 0 ? pairs % sms : 0;
     if (rem > 0 && 2 * rem <= sms) blocks = pairs + rem;
+  }
+  if constexpr (LAYOUT == kGrouped) {
+    // A CTA without a pair costs its SM 1.5 us. To find the pairs that exist
+    // costs every CTA 1.1 us and about 0.6 more per 100 sequences (grids with
+    // and without empty CTAs; 8 to 1024 sequences), so it is done where three
+    // quarters as many CTAs or more would be empty: 63 prompts of 100 tokens
+    // and one of 8192, 16/4 heads, d 128: 548 -> 259 us; 255 of 60 and one of
+    // 4096, 32/8 heads: 1487 -> 348; 9 of up to 2500, 12/4 heads, d 64: 61.7
+    // -> 59.7.
+    const long long cols = a.s.H / a.qt.P;
+    const long long real = std::min<long long>(pairs, (a.pk.total_q / (2 * tok) + a.s.B) * cols);
+    if (4 * (pairs - real) > real * (3 + a.s.B / 64)) {
+      const long long kv = static_cast<long long>(a.pk.total_k) * a.s.Hk * D * 4;
+      const long long half = std::max(current_l2_bytes() / 2, 1LL);
+      const long long groups = std::min<long long>(a.s.B, std::max(1LL, (kv + half - 1) / half));
+      a.group_seqs = static_cast<int>((a.s.B + groups - 1) / groups);
+      kern = fa_fwd_kernel<D, CAUSAL, LAYOUT, true>;
+      if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES)) != cudaSuccess)
+        return e;
+      blocks = real;
+    }
   }
   if (blocks > 0x7fffffffLL || 2 * pairs - blocks < 0) return cudaErrorInvalidConfiguration;
   mark(marks, true, 0, stream);

@@ -51,6 +51,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // Programmatic dependent launch. A kernel launched with programmatic stream
 // serialization may start before the previous kernel on its stream has
 // finished; griddep_wait() blocks until that kernel has completed and its

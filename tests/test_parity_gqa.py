@@ -106,6 +106,38 @@ def test_forward_equals_repeated_key_heads_bit_for_bit(H, Hk, d, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk,d,causal,lens,extra", [
+    (16, 4, 128, True, [3000] + [50 + i for i in range(40)], 0),          # several passes over 32 sequences
+    (6, 2, 64, False, [0, 0, 1, 2600, 0, 300, 77, 1], 0),
+    (8, 8, 64, True, [7, 1500, 0, 63, 64, 65], 40),                       # more keys than queries, full heads
+    (4, 1, 128, True, [1 + 13 * i % 61 for i in range(300)] + [2000], 0),
+    (8, 1, 128, True, [20000, 30000, 9, 100, 26000, 5, 900, 40000], 0),   # K and V of the batch past half the L2
+])
+def test_short_prompts_beside_long_ones(H, Hk, d, causal, lens, extra):
+    """Batches whose grid holds only the tiles that exist: every row as with
+    repeated key heads, bit for bit, and the same again when the longest
+    length named is larger than the batch's."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(43)
+    lens_k = [n + extra for n in lens]
+    cq, ck = (torch.from_numpy(cum(n)).cuda() for n in (lens, lens_k))
+    T, Tk = sum(lens), sum(lens_k)
+    q = torch.randn(T, H, d, device="cuda", generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(Tk, Hk, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    kr, vr = (t.repeat_interleave(H // Hk, dim=1) for t in (k, v))
+    ro, rl = binding.attention_forward_varlen(q, kr, vr, cq, ck, max(lens), max(lens_k), d ** -0.5, causal)
+    for longest in (max(lens), min(5 * max(lens), T)):
+        o = torch.full_like(q, float("nan"))
+        lse = torch.full((H, T), float("nan"), device="cuda")
+        binding.fa_fwd_varlen_gqa(q, k, v, o, lse, cq, ck, longest, max(lens_k), d ** -0.5, causal)
+        torch.cuda.synchronize()
+        assert binding.fa_check_status() == binding.FA_OK
+        assert torch.equal(o.view(torch.int16), ro.view(torch.int16))
+        assert torch.equal(lse, rl)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("deterministic", [False, True])
