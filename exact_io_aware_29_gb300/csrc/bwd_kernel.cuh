@@ -318,10 +318,10 @@ __device__ __forceinline__ BwdWork bwd_work(const BwdArgs& args, int item) {
   // every head are therefore kept back until all groups have had their others.
   // And key blocks count from the end of their own sequence, so that in a
   // ragged batch too the work goes down from item to item. Forward + backward,
-  // d 128: 8 sequences of 1024..4096 tokens, 16/4 heads 1427 -> 1384 us; 8 of
-  // 2500, 16/2 heads 960 -> 830; 12 of up to 2048, 32/8 heads 608 -> 589; where
-  // there are many items (8 of 8192, 32/8 heads) it changes nothing. All heads
-  // in one group balance as well, but overflow the L2 (8 of 8192: 12.9 -> 17 ms).
+  // d 128: 8 sequences of 1024..4096 tokens, 16/4 heads 1427 -> 1384 us; 12 of
+  // up to 2048, 32/8 heads 608 -> 589; where there are many items (8 of 8192,
+  // 32/8 heads) it changes nothing. All heads in one group balance as well, but
+  // overflow the L2 (8 of 8192: 12.9 -> 15.3 ms).
   const int heads = LAYOUT == kGrouped ? sh.Hk : sh.H;
   const int BH = sh.B * heads;
   constexpr bool LATE = LAYOUT == kGrouped && CAUSAL && !DET;
@@ -1346,7 +1346,13 @@ static cudaError_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, co
     const long long share = LAYOUT == kGrouped ? args.s.H / args.s.Hk : 1;
     const long long per_head = static_cast<long long>(Npad) * D * 8 * share;
     const long long l2 = l2_cache_bytes();
-    const long long g = l2 > 0 ? l2 / per_head : 16;
+    long long g = l2 > 0 ? l2 / per_head : 16;
+    // Up to 16 key heads in the batch run as one group: nine or more CTAs then
+    // go through each head's Q and dO at the same time, so the L2 serves them
+    // anyway, and the heaviest items all come first (d 128: 8 sequences of 2500
+    // tokens, 16/2 heads 830 -> 780 us; 4 of 4096, 16/2 heads 1018 -> 924; one
+    // of 16384, 32/8 heads the same; with 32 key heads it costs up to 5 %).
+    if (LAYOUT == kGrouped && BH / share <= 16) g = 16;
     a.heads_per_group = balanced_heads_per_group(BH / share, g);
     // The late key blocks (bwd_work): as many as hold a quarter of the
     // heaviest item's pairs per SM, all heads together, and groups that keep
