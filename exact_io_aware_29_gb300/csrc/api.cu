@@ -270,11 +270,13 @@ void shared_plan(fa::SharedArgs* a) {
   const int G = a->H / a->Hk;
   const long long group_rows = static_cast<long long>(a->max_group) * G;
   a->seq_blocks = (G + 63) / 64;
-  // Items of about 4 us to start and end and 0.7 us per tile, two at a time on
-  // each of 152 SMs: prefixes cut into about 152 items, sequences into about
-  // 608 (their lengths differ). Measured on 40 sequences of up to 700 tokens
-  // behind six prefixes of up to 4000 (d = 64): 19.5 us with 152, 21.4 with 304
-  // and 24.5 with 608 prefix items; own parts in 1024 items 1.4 us slower.
+  // Items of about 4 us to start and end and 0.7 us per tile, on each of 152 SMs
+  // two at a time (d 128) or four (d 64): prefixes cut into about 152 or 304
+  // items, sequences into about 608 (their lengths differ). Measured at d 64 on
+  // 40 sequences of up to 700 tokens behind six prefixes of up to 4000: 17.6 us
+  // with 304 prefix items, 22.5 with 152, 21.3 with 608 (two per SM with six
+  // stages: 19.6 with 152, 21.4 with 304); 64 sequences of 4096 own tokens, 32/8
+  // heads: 88 us, 94.6 two per SM; own parts in 1216 items 1 to 5 us slower.
   split_keys(static_cast<long long>(a->B) * a->Hk * a->seq_blocks, a->max_seq_len, 608, &a->seq_chunk,
              &a->seq_splits);
   // More than one 16-row block of the streaming kernel: 128-row tiles. Measured
@@ -284,7 +286,8 @@ void shared_plan(fa::SharedArgs* a) {
   // 40.9 in tiles, 20.8 / 34.5 / 87.7 streamed.
   a->prefix_tiles = group_rows > 16;
   if (!a->prefix_tiles) {
-    split_keys(static_cast<long long>(a->P) * a->Hk, a->max_prefix_len, 152, &a->prefix_chunk, &a->prefix_splits);
+    split_keys(static_cast<long long>(a->P) * a->Hk, a->max_prefix_len, a->D == 64 ? 304 : 152,
+               &a->prefix_chunk, &a->prefix_splits);
     return;
   }
   // 128-row tiles, two per CTA and one CTA per SM: the number of splits whose

@@ -36,7 +36,8 @@ struct SharedCfg {
   static constexpr int BOX_BYTES = TK * 128;          // 64 rows x 64 bf16, 128B-swizzled
   static constexpr int TILE_BYTES = BOXES * BOX_BYTES;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K tile, then V tile
-  static constexpr int STAGES = D == 128 ? 3 : 6;     // 96 KB in flight; two CTAs per SM
+  static constexpr int STAGES = 3;                    // two CTAs per SM with 96 KB each, four with 48 (d 64)
+  static constexpr int CTAS = D == 128 ? 2 : 4;       // per SM (the registers allow no more at d 128)
   static constexpr int CWARPS = 4;                    // consumer warps
   static constexpr int ROWS = 16 * CWARPS;            // most rows of an item
   static constexpr int THREADS = (CWARPS + 1) * 32;
@@ -132,7 +133,7 @@ __device__ __forceinline__ bool shared_item(const SharedArgs& a, int id, SharedI
 }
 
 template <int D>
-__global__ void __launch_bounds__(SharedCfg<D>::THREADS, 2)
+__global__ void __launch_bounds__(SharedCfg<D>::THREADS, SharedCfg<D>::CTAS)
     fa_decode_shared_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const SharedArgs a) {
   using C = SharedCfg<D>;
