@@ -408,6 +408,7 @@ __device__ __forceinline__ void find_pair(const FwdGroupedArgs& args, int cols, 
       }
       i -= __popc(has);
     }
+    bh = min(max(bh, 0), B * cols - 1);  // (offsets that break the contract can make the counts overflow)
     return;
   }
 }
