@@ -123,6 +123,11 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
   bool in_range;
   SeqView sv;
   if constexpr (LAYOUT == kGrouped) {
+    // Nothing is read or written before the kernel in front of this one has
+    // finished, whatever it is: it may be the one that writes the offsets, or
+    // still read a tensor whose memory has since become this workspace.
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();
     // Blocks that share a tile first, then the heads: their O and dO rows lie side by side.
     constexpr int SHARE = 128 / (RPP * PASSES);
     const int part = blockIdx.x % SHARE, h = blockIdx.x / SHARE % a.s.H;
@@ -154,10 +159,13 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
       z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  griddep_wait();  // O and LSE come from the forward
-  if (LAYOUT == kGrouped && !in_range) return;
-  if (LAYOUT != kGrouped) sv = seq_view<LAYOUT>(a.pk, a.kv_lens, static_cast<int>(bh / a.s.H), N, a.s.Nk);
+  if constexpr (LAYOUT == kGrouped) {
+    if (!in_range) return;
+  } else {
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    griddep_wait();  // O and LSE come from the forward
+    sv = seq_view<LAYOUT>(a.pk, a.kv_lens, static_cast<int>(bh / a.s.H), N, a.s.Nk);
+  }
   uint4 o4[PASSES], d4[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
