@@ -589,7 +589,8 @@ def attention_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len
                                    stream=None):
     """Allocates O and LSE, then calls fa_decode_shared_prefix. Returns (O, LSE)."""
     torch = _load_torch()
-    o, lse = _alloc(stream, lambda: (torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)))
+    o, lse = _alloc(stream, lambda: (torch.empty_like(q),
+                                     torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)))
     fa_decode_shared_prefix(q, k_cache, v_cache, o, lse, prefix_table, prefix_lens, cu_prefix_seqs, block_table,
                             seq_lens, max_group, max_prefix_len, max_seq_len, scale, workspace, stream)
     return o, lse

@@ -294,7 +294,8 @@ void shared_plan(fa::SharedArgs* a) {
   // waves take the least time, a CTA costing its 128-key blocks and about
   // three more to start and to write its part.
   const fa::QTile qt = q_tile(G);
-  const long long base = static_cast<long long>(a->P) * (a->H / qt.P) * ((a->max_group + 2 * qt.tok - 1) / (2 * qt.tok));
+  const int pairs = (a->max_group + 2 * qt.tok - 1) / (2 * qt.tok);
+  const long long base = static_cast<long long>(a->P) * (a->H / qt.P) * pairs;
   const long long blocks = (static_cast<long long>(a->max_prefix_len) + 127) / 128;
   long long best = -1;
   for (long long ns = 1; ns <= std::min<long long>(blocks, 152); ++ns) {

@@ -872,7 +872,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 const int q = q4 * 2 + e;
                 const int qa = h * 64 + c * 32 + 2 * q;  // query column within the block
                 float xa, xb;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1])), sl2x2, lp[e]), xa, xb);
+                const uint64_t s2 = f2_pack(__uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]));
+                f2_unpack(f2_fma(s2, sl2x2, lp[e]), xa, xb);
                 float pa = ex2(xa);
                 float pb = ex2(xb);
                 if constexpr (decltype(with_mask)::value) {

@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, SharedCfg<D>::CTAS)
       }
       // Do not leave with copies in flight (matters only after an abort, when
       // the consumers stopped waiting; every issued copy lands).
-      for (int t = max(0, issued - C::STAGES); t < issued; ++t) mbar_wait_drain(&full[t % C::STAGES], (t / C::STAGES) & 1);
+      for (int t = max(0, issued - C::STAGES); t < issued; ++t)
+        mbar_wait_drain(&full[t % C::STAGES], (t / C::STAGES) & 1);
     }
     return;
   }
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, SharedCfg<D>::CTAS)
   for (int j = 0; j < D / 8; ++j) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float2*>(&red_o[(warp * 16 + gr + 8 * i) * D + j * 8 + gc]) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+      *reinterpret_cast<float2*>(&red_o[(warp * 16 + gr + 8 * i) * D + j * 8 + gc]) =
+          make_float2(o[j][2 * i], o[j][2 * i + 1]);
   }
   if ((lane & 3) == 0) {
 #pragma unroll
@@ -337,7 +339,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, SharedCfg<D>::CTAS)
       const float f = ex2(mw - M);
       const float4 x = *reinterpret_cast<const float4*>(&red_o[(w * 16 + (r & 15)) * D + c]);
       sum = fmaf(red_ml[(w * 16 + (r & 15)) * 2 + 1], f, sum);
-      acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y), acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
+      acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const size_t at = static_cast<size_t>(q_index(r)) * nparts + it.slot;
@@ -419,7 +422,8 @@ __global__ void __launch_bounds__(128) fa_decode_shared_join_kernel(const Shared
     for (int k = 0; k < CPL; ++k) acc[k] += red[w][lane * CPL + k];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + static_cast<size_t>(blockIdx.x) * D + lane * CPL);
+  uint16_t* row = static_cast<uint16_t*>(a.o) + static_cast<size_t>(blockIdx.x) * D;
+  uint32_t* out = reinterpret_cast<uint32_t*>(row + lane * CPL);
 #pragma unroll
   for (int k = 0; k < CPL; k += 2) out[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
   if (lane == 0) a.lse[blockIdx.x] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;

@@ -532,7 +532,8 @@ __device__ __forceinline__ int fwd_load_kv_range(const FwdArgsT<LAYOUT>& args, c
 // wait gave up).
 template <int D, int LAYOUT>
 __device__ __forceinline__ int fwd_load_kv(const FwdArgsT<LAYOUT>& args, const FwdShared<D>& sm,
-                                           const FwdCtaT<LAYOUT>& c, const CUtensorMap* tmK, const CUtensorMap* tmV, int g0, int n) {
+                                           const FwdCtaT<LAYOUT>& c, const CUtensorMap* tmK,
+                                           const CUtensorMap* tmV, int g0, int n) {
   return fwd_load_kv_range<D, LAYOUT>(args, sm, c, tmK, tmV, g0, 0, 2 * n);
 }
 
@@ -713,8 +714,8 @@ __device__ __forceinline__ bool fwd_softmax_pass(const FwdShared<D>& sm, const C
 // Epilogue of one row: O = acc / l (times ``unscale``) as bf16 and LSE.
 // Returns the row's largest |O| (NaN if an element is NaN).
 template <int D, int LAYOUT>
-__device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, const FwdCtaT<LAYOUT>& c, int r, uint32_t tO, bool have_o,
-                                              float m_used, float l, float unscale, int rr) {
+__device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, const FwdCtaT<LAYOUT>& c, int r,
+                                              uint32_t tO, bool have_o, float m_used, float l, float unscale, int rr) {
   const bool valid = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || rr < args.qt.tok * args.qt.P);
   // Flattened query head of the row (grouped: row rr of the tile is head hh + rr % P).
   const int bh = tile_of_heads(LAYOUT) ? c.hh + rr % args.qt.P : c.bh;
@@ -785,8 +786,8 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, cons
 // + 2 n_r) the pass itself; every barrier continues from its first-pass phase.
 // ---------------------------------------------------------------------------
 template <int D, bool CAUSAL, int LAYOUT>
-__device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtensorMap* tmV, FwdArgsT<LAYOUT> args, FwdCtaT<LAYOUT> c,
-                                           uint32_t mask) {
+__device__ __noinline__ void fwd_bf16_pass(const CUtensorMap* tmK, const CUtensorMap* tmV, FwdArgsT<LAYOUT> args,
+                                           FwdCtaT<LAYOUT> c, uint32_t mask) {
   using C = FwdCfg<D>;
   const FwdShared<D> sm(reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(fwd_smem_base()) + 1023) & ~uintptr_t(1023)));

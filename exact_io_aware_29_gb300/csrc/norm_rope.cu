@@ -32,7 +32,9 @@ __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t swap_halves(uint32_t w) { return __funnelshift_l(w, w, 16); }
 
-__device__ __forceinline__ void words(const uint4& v, uint32_t (&w)[4]) { w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w; }
+__device__ __forceinline__ void words(const uint4& v, uint32_t (&w)[4]) {
+  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -210,7 +212,8 @@ __global__ void __launch_bounds__(256, 4) fa_norm_rope_kernel(const NormRopeArgs
     RowStream<D, B, 1> rs(a, ring, phase, u0);
     while (u0 < rs.end) {
       const Unit t = rs.unit_at(u0);
-      uint16_t* dst = static_cast<uint16_t*>(phase ? a.yk : a.yq) + (t.token * (phase ? a.Hk : a.H) + t.head) * D + l * 8;
+      uint16_t* dst =
+          static_cast<uint16_t*>(phase ? a.yk : a.yq) + (t.token * (phase ? a.Hk : a.H) + t.head) * D + l * 8;
       Rotation<LPR, INTER> rot;
       rot.load(a, t.token, lane);
       {
@@ -313,7 +316,8 @@ __global__ void __launch_bounds__(256, 2) fa_norm_rope_bwd_kernel(const NormRope
             dw[phase][2 * k + 1] = fmaf(du[2 * k + 1], x1 * rw, dw[phase][2 * k + 1]);
             y[k] = pack_bf16x2(r * fmaf(-x0, m, du[2 * k] * lo_f(w[k])), r * fmaf(-x1, m, du[2 * k + 1] * hi_f(w[k])));
           }
-          if (on) *reinterpret_cast<uint4*>(dst + static_cast<long long>(i0 + i) * D) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (on)
+            *reinterpret_cast<uint4*>(dst + static_cast<long long>(i0 + i) * D) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       if (phase == 0 && u0 + GROUPS > rs.nq) break;  // the straddling step again, for its k units
