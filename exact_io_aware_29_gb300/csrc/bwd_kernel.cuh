@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
   int n;
   bool in_range;
   SeqView sv;
+  // Nothing is read or written before the kernel in front of this one has
+  // finished, whatever it is: it may be the one that writes the offsets, or a
+  // forward that still reads, or writes, a tensor whose memory has since become
+  // this workspace. (What a dependent launch saves is the launch itself.)
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
   if constexpr (LAYOUT == kGrouped) {
-    // Nothing is read or written before the kernel in front of this one has
-    // finished, whatever it is: it may be the one that writes the offsets, or
-    // still read a tensor whose memory has since become this workspace.
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();
     // Blocks that share a tile first, then the heads: their O and dO rows lie side by side.
     constexpr int SHARE = 128 / (RPP * PASSES);
     const int part = blockIdx.x % SHARE, h = blockIdx.x / SHARE % a.s.H;
@@ -145,12 +146,11 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
     in_range = row < rows;
     bh = in_range ? row / Npad : 0;
     n = in_range ? static_cast<int>(row % Npad) : 0;
+    sv = seq_view<LAYOUT>(a.pk, a.kv_lens, static_cast<int>(bh / a.s.H), N, a.s.Nk);
     if (tid < rows / 128) a.dq_turn[tid] = 0u;
   }
-  // Workspace state first: it depends on nothing the forward writes, so with
-  // a programmatic launch it overlaps the forward's last CTAs. Counters of the
-  // deterministic order (one per 128-row block) and the ticket, then the
-  // accumulator, which has exactly D floats per padded row.
+  // Counters of the deterministic order (one per 128-row block, above) and the
+  // ticket, then the accumulator, which has exactly D floats per padded row.
   if (tid == 0) *a.ticket = 0u;
   if (in_range) {
 #pragma unroll
@@ -160,13 +160,7 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
       z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if constexpr (LAYOUT == kGrouped) {
-    if (!in_range) return;
-  } else {
-    if (threadIdx.x == 0) griddep_launch_dependents();
-    griddep_wait();  // O and LSE come from the forward
-    sv = seq_view<LAYOUT>(a.pk, a.kv_lens, static_cast<int>(bh / a.s.H), N, a.s.Nk);
-  }
+  if (LAYOUT == kGrouped && !in_range) return;
   uint4 o4[PASSES], d4[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {

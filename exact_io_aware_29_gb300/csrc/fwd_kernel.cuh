@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(384, 1)
   c.tmem = *sm.tmem_slot;
   // A backward pre-pass launched programmatically after this kernel may start
   // once every CTA of this grid is running (it waits for this grid to finish
-  // before it reads O and LSE).
+  // before it reads O and LSE or writes anything).
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
