@@ -21,7 +21,9 @@
 //   as the sum of two bf16 numbers (hi = bf16(p), lo = bf16(p - hi): relative
 //   error 2^-17), so P costs no more accuracy than the fp32 sums around it.
 // Every item writes a normalised partial O and the log2 of its sum; a second
-// kernel joins the parts of each row in a fixed order (deterministic).
+// kernel joins the parts of each row in a fixed order (deterministic). Only a
+// sum of exactly zero (no keys) is left out of a join: a NaN logit makes its
+// part's sum NaN and the row's O and LSE with it, however its keys are split.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -77,6 +79,13 @@ __device__ __forceinline__ uint32_t unit_off(int r, int u) {
 __device__ __forceinline__ void split_bf16(float p0, float p1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(p0, p1);
   lo = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// max(a, b), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 }  // namespace
@@ -334,18 +343,18 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, SharedCfg<D>::CTAS)
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = b; w < C::CWARPS; w += nb) {
-      const float mw = red_ml[(w * 16 + (r & 15)) * 2];
-      if (mw == -INFINITY) continue;
+      const float mw = red_ml[(w * 16 + (r & 15)) * 2], lw = red_ml[(w * 16 + (r & 15)) * 2 + 1];
+      if (lw == 0.f) continue;  // no keys (NaN logits alone leave mw at -inf, too, but make lw NaN)
       const float f = ex2(mw - M);
       const float4 x = *reinterpret_cast<const float4*>(&red_o[(w * 16 + (r & 15)) * D + c]);
-      sum = fmaf(red_ml[(w * 16 + (r & 15)) * 2 + 1], f, sum);
+      sum = fmaf(lw, f, sum);
       acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
       acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const size_t at = static_cast<size_t>(q_index(r)) * nparts + it.slot;
     *reinterpret_cast<float4*>(a.part_o + at * D + c) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (c == 0) a.part_lse[at] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+    if (c == 0) a.part_lse[at] = sum == 0.f ? -INFINITY : M + log2f(sum);
   }
   if (waits) griddep_wait();
 }
@@ -383,13 +392,13 @@ __global__ void __launch_bounds__(128) fa_decode_shared_join_kernel(const Shared
   auto part = [&](int i) { return at0 + (i < np ? i : a.prefix_splits + i - np); };
   griddep_wait();
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_lse[part(i)]);
+  for (int i = lane; i < n; i += 32) M = max_nan(M, a.part_lse[part(i)]);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
   float sum = 0.f, acc[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
-  for (int i0 = 0; i0 < n && M > -INFINITY; i0 += 128) {
+  for (int i0 = 0; i0 < n && M != -INFINITY; i0 += 128) {
     // This warp's parts i0 + warp + 4 j, j < 32: lane j holds the weight of the j-th.
     const int mine = i0 + warp + 4 * lane;
     const float w = mine < n ? ex2(a.part_lse[part(mine)] - M) : 0.f;
@@ -421,12 +430,12 @@ __global__ void __launch_bounds__(128) fa_decode_shared_join_kernel(const Shared
 #pragma unroll
     for (int k = 0; k < CPL; ++k) acc[k] += red[w][lane * CPL + k];
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* row = static_cast<uint16_t*>(a.o) + static_cast<size_t>(blockIdx.x) * D;
   uint32_t* out = reinterpret_cast<uint32_t*>(row + lane * CPL);
 #pragma unroll
   for (int k = 0; k < CPL; k += 2) out[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0) a.lse[blockIdx.x] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[blockIdx.x] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 template <int D>

@@ -721,7 +721,8 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, cons
   const int bh = tile_of_heads(LAYOUT) ? c.hh + rr % args.qt.P : c.bh;
   const float inv = (l > 0.f) ? 1.f / l : 0.f;
   if constexpr (LAYOUT == kShared) {
-    // A partial result: normalised O in fp32 and the base-2 log of the sum.
+    // A partial result: normalised O in fp32 and the base-2 log of the sum (NaN
+    // for a NaN sum: only a part without keys is left out when the parts are joined).
     const size_t at = (static_cast<size_t>(c.sv.q_start + r) * args.dec.H + bh) *
                           (args.dec.prefix_splits + args.dec.seq_splits) + c.slot;
     float omax = 0.f;
@@ -739,7 +740,7 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, cons
         if (valid) out[i] = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
-    if (valid) args.dec.part_lse[at] = (l > 0.f) ? m_used + log2f(l) - 7.0f : -INFINITY;
+    if (valid) args.dec.part_lse[at] = (l == 0.f) ? -INFINITY : m_used + log2f(l) - 7.0f;
     return omax;
   }
   // Output row r of this sequence: [B,H,N,d] or packed [total,H,d]; LSE
@@ -995,7 +996,10 @@ __global__ void __launch_bounds__(384, 1)
       // Range check: a row that needs the bf16 pass flags its tile (what was
       // written is then overwritten).
       // Rows of a grouped tile past its tok * P hold nothing.
-      const bool real = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || wq * 32 + lane < args.qt.tok * args.qt.P);
+      bool real = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || wq * 32 + lane < args.qt.tok * args.qt.P);
+      // A row with a NaN logit stays NaN whatever P is rounded to: it does not
+      // cost the tile's other rows their f16 P.
+      if (LAYOUT == kShared) real = real && l == l;
       if (ok && real && row_needs_bf16_pass(omax, l)) atomicOr(const_cast<uint32_t*>(sm.redo), 1u << t);
     }
   }

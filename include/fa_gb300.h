@@ -256,7 +256,8 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
  * Without sharing (every prefix_lens[p] = 0, or sequences of no prefix) it is
  * a paged decoding step with grouped heads.
  *   q, o           device bf16 [B, H, d];  lse  device fp32 [B, H] (natural log;
- *                  -inf and O = 0 for a sequence with no keys at all).
+ *                  -inf and O = 0 for a sequence with no keys at all, and for
+ *                  nothing else: a NaN logit gives NaN in both).
  *   k_cache, v_cache  device bf16 [num_blocks, block_size, H_kv, d].
  *   prefix_table   device int32 [n_prefix, max_prefix_blocks];  prefix_lens
  *                  device int32 [n_prefix], each in [0, max_prefix_len].
