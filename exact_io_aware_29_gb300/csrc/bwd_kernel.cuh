@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
       float nl2 = -INFINITY;  // 2^(x + nl2) = 0: the row contributes nothing
       if (n + i * RPP < sv.Lq) {
         const float l = a.lse[lse_index<LAYOUT>(a.pk, a.s, sv, static_cast<int>(bh), n + i * RPP)];
-        if (l > -INFINITY) nl2 = LAYOUT == kGrouped ? fmaf(-l, kLog2e, kPScaleLog2) : -l * kLog2e;
+        if (LAYOUT == kGrouped ? l != -INFINITY : l > -INFINITY)  // grouped: a NaN row's P is NaN
+          nl2 = LAYOUT == kGrouped ? fmaf(-l, kLog2e, kPScaleLog2) : -l * kLog2e;
       }
       a.lse2[row + i * RPP] = nl2;
     }

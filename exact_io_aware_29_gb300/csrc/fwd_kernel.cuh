@@ -772,9 +772,12 @@ __device__ __forceinline__ float fwd_epilogue(const FwdArgsT<LAYOUT>& args, cons
         orow[cc * 4 + v4] = make_uint4(w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2], w[4 * v4 + 3]);
     }
   }
+  // -inf for a row without a visible key; grouped layout: for no other, a NaN sum
+  // gives a NaN LSE beside the NaN O.
+  const bool has_lse = LAYOUT == kGrouped ? l != 0.f : l > 0.f;
   if (valid)
     args.lse[lse_index<LAYOUT>(args.pk, args.s, c.sv, bh, r)] =
-        (l > 0.f) ? (m_used + log2f(l) - 7.0f) * kLn2 : -INFINITY;
+        has_lse ? (m_used + log2f(l) - 7.0f) * kLn2 : -INFINITY;
   return omax;
 }
 
@@ -999,7 +1002,7 @@ __global__ void __launch_bounds__(384, 1)
       bool real = r < c.sv.Lq && (!tile_of_heads(LAYOUT) || wq * 32 + lane < args.qt.tok * args.qt.P);
       // A row with a NaN logit stays NaN whatever P is rounded to: it does not
       // cost the tile's other rows their f16 P.
-      if (LAYOUT == kShared) real = real && l == l;
+      if (tile_of_heads(LAYOUT)) real = real && l == l;
       if (ok && real && row_needs_bf16_pass(omax, l)) atomicOr(const_cast<uint32_t*>(sm.redo), 1u << t);
     }
   }

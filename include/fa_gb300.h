@@ -195,6 +195,7 @@ int fa_bwd_varlen_deterministic(const void* q, const void* k, const void* v, con
  * Sequences longer than max_seqlen_* or reaching past total_* are cut there
  * (check mode rejects them). fa_bwd_varlen_gqa_deterministic sums dQ in a
  * fixed order (bitwise repeatable), like fa_bwd_varlen_deterministic.
+ * A row with a NaN logit gets a NaN O and a NaN LSE (-inf: no visible key).
  * Errors: as for the entry points above; FA_ERR_INVALID also when H is not a
  * multiple of H_kv.
  */
