@@ -1039,7 +1039,8 @@ static int norm_rope_args(fa::NormRopeArgs* a, const void* q, const void* k, con
                           const void* k_weight, const float* cos, const float* sin, const int* positions, int T, int H,
                           int H_kv, int d, int rot, int max_pos, long long q_stride, long long k_stride, float eps,
                           int interleaved) {
-  if (!q || !k || !q_weight || !k_weight || !cos || !sin || !positions) return FA_ERR_INVALID;
+  if (!q || !k || !q_weight || !k_weight || !positions) return FA_ERR_INVALID;
+  if (rot != 0 && (!cos || !sin)) return FA_ERR_INVALID;  // without a rotation the tables are empty and not read
   if (H_kv < 1 || max_pos < 1 || rot < 0 || rot > d) return FA_ERR_INVALID;
   if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID;
   int st = check_shape(T, H, 1, d, 1.f);
@@ -1048,9 +1049,10 @@ static int norm_rope_args(fa::NormRopeArgs* a, const void* q, const void* k, con
   if (q_stride < static_cast<long long>(H) * d || k_stride < static_cast<long long>(H_kv) * d) return FA_ERR_INVALID;
   if (rot % 16 != 0 || q_stride % 8 != 0 || k_stride % 8 != 0) return FA_ERR_UNSUPPORTED;
   if (q_stride > (1LL << 40) / T || k_stride > (1LL << 40) / T) return FA_ERR_UNSUPPORTED;
-  const void* ptrs[] = {q, k, q_weight, k_weight, cos, sin};
+  const void* ptrs[] = {q, k, q_weight, k_weight};
   for (const void* p : ptrs)
     if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  if (rot != 0 && (!aligned16(cos) || !aligned16(sin))) return FA_ERR_UNSUPPORTED;
   *a = fa::NormRopeArgs{};
   a->q = q;
   a->k = k;

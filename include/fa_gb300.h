@@ -333,7 +333,8 @@ int fa_fwd_fp8(const void* q8, const void* k8, const void* v8t, const float* q_s
  *                  [t * stride + h * d + e] (strides in elements, multiples of
  *                  8, >= heads * d), so both can be parts of a fused projection.
  *   q_weight, k_weight  device bf16 [d].
- *   cos, sin       device fp32 [max_pos, rot / 2], 16-byte aligned.
+ *   cos, sin       device fp32 [max_pos, rot / 2], 16-byte aligned (rot = 0:
+ *                  not read, may be NULL).
  *   positions      device int32 [T], in [0, max_pos) (check mode rejects others
  *                  on the host; otherwise they are clamped on the device).
  *   q_out, k_out   device bf16 [T, H, d] and [T, H_kv, d], contiguous.
