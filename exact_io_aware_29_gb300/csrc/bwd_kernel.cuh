@@ -368,6 +368,47 @@ __device__ __forceinline__ BwdWork bwd_work(const BwdArgs& args, int item) {
   return w;
 }
 
+// Packed layout, the 256 key-row threads (the grouped one: warp 15). The last
+// query and key blocks of a sequence also hold rows of the next one, which may
+// hold anything: a NaN there times the zero that P and dS have for those rows
+// would be a NaN in dK, dV and dQ. They are zeroed in shared memory once S^T has
+// been read out of Q and K and nothing has read dO or V yet: rows of Q (its
+// slot) and dO from q_rows on, of K and V (in either buffer) from k_rows on.
+// False if a wait gave up. Out of line, so that it takes none of the loop's
+// registers. (Backward, 16 sequences of 512..8192 tokens, 16 heads: d 128 3378 us
+// without cleaning, 3141 with it and the unmasked copy of the P phase, 3660 with
+// warp 15 as in the grouped layout, where it is the faster form; d 64 2619 ->
+// 2358; 20 sequences of 100..271: 74 -> 78.)
+template <int D>
+__device__ __noinline__ bool bwd_clean_tiles(uint8_t* smem, int slot, int q_rows, int k_rows, uint32_t do_phase,
+                                             uint32_t v_phase) {
+  using C = BwdCfg<D>;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t *do_full = bars + 5, *v_full = bars + 16;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + C::NUM_BARS) + 1;
+  bool ok = true;
+  auto clean = [&](int off, int rows) {
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = threadIdx.x - 64; e < (128 - rows) * 8; e += 256) {
+#pragma unroll
+      for (int c = 0; c < C::CHUNKS; ++c)
+        *reinterpret_cast<uint4*>(smem + off + c * C::SUB + rows * 128 + e * 16) = z;
+    }
+  };
+  if (q_rows < C::BM) {
+    ok = mbar_wait(do_full, do_phase, abort_flag);
+    clean(C::OFF_Q + slot * C::TILE, q_rows);
+    clean(C::OFF_DO, q_rows);
+  }
+  if (k_rows < C::BN) {
+    ok = ok && mbar_wait(v_full, v_phase, abort_flag);
+    clean(C::OFF_K, k_rows);
+    clean(C::OFF_V, k_rows);
+  }
+  fence_proxy_async_smem();
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Persistent: one CTA per SM takes work items from a global ticket counter
 // until none is left. Every mbarrier is used either once per block pair (its
 // phase is the pair's index p, counted over all of this CTA's items) or once
@@ -881,6 +922,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 float pb = ex2(xb);
                 if constexpr (decltype(with_mask)::value) {
                   if (!kvalid) pa = pb = 0.f;
+                  if (LAYOUT == kPacked) {  // rows past the sequence's queries, whatever they hold
+                    if (qa >= wk.sv.Lq - qb * C::BM) pa = 0.f;
+                    if (qa + 1 >= wk.sv.Lq - qb * C::BM) pb = 0.f;
+                  }
                   if (diag) {
                     if (qa < lim) pa = 0.f;
                     if (qa + 1 < lim) pb = 0.f;
@@ -901,17 +946,24 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             if constexpr (LAYOUT != kGrouped) tmem_st16(tr + h * 64 + c * 16, pb16);
           }
         };
-        // Grouped layout: most pairs have no masked entry (every key is the
+        // Packed layouts: most pairs have no masked entry (every key is the
         // sequence's and seen by every query of the block); they take a copy of
         // the code without the masks (8 sequences of up to 4096 tokens, 16/4
-        // heads, d 128, forward + backward: 1572 -> 1419 us). The compiler does
-        // the same for the fixed layout's diagonal by itself.
-        const bool masked = LAYOUT != kGrouped || wk.key0 + C::BN > wk.sv.Lk ||
+        // heads, d 128, grouped, forward + backward: 1572 -> 1419 us). The
+        // compiler does the same for the fixed layout's diagonal by itself.
+        const bool masked = LAYOUT == kFixed || wk.key0 + C::BN > wk.sv.Lk ||
+                            (LAYOUT == kPacked && (qb + 1) * C::BM > wk.sv.Lq) ||
                             (CAUSAL && wk.key0 + C::BN - 1 - wk.sv.shift - qb * C::BM > 0);
         if (masked)
           p_phase(std::true_type{});
         else
           p_phase(std::false_type{});
+        // Tiles that reach past their sequence are cleaned before any product but
+        // S^T reads them: dV and dP^T, then dK and dQ, follow p_ready.
+        if (LAYOUT == kPacked && ((qb + 1) * C::BM > wk.sv.Lq || (it == 0 && wk.key0 + C::BN > wk.sv.Lk))) {
+          ok = bwd_clean_tiles<D>(smem, slot, wk.sv.Lq - qb * C::BM, it == 0 ? wk.sv.Lk - wk.key0 : C::BN, p & 1, ci & 1);
+          if (!ok) break;
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_ready);
