@@ -1077,26 +1077,25 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // of the item has completed), written there in the same swizzled key-major
         // layout by its key-row thread, then copied to global memory as whole row
         // segments by all 256 key-row threads (8 threads per 128-byte segment).
-        // Fixed layout: keys past kv_len (< N) get their zero gradients written
-        // (the accumulators hold zero there: every P^T and dS^T entry of such a
-        // key is masked); packed layout: rows past this sequence belong to the
-        // next one.
+        // Fixed layout only: keys past kv_len (< N) get their zero gradients
+        // written (the accumulators hold zero there: every P^T and dS^T entry of
+        // such a key is masked).
         const int ktid = threadIdx.x - 64;  // 0..255 over the key-row warps
         uint8_t* stage = smem + C::OFF_DS;
         auto srow = [&](int row, int g) {  // 16-byte unit g (8 columns) of key row `row`
           return stage + (g >> 3) * C::SUB + row * 128 + (((g & 7) ^ (row & 7)) << 4);
         };
-  #pragma unroll
+#pragma unroll
         for (int which = 0; which < 2; ++which) {
           const uint32_t tacc = (which == 0 ? tDV : tDK) + lo;
-          const float mul = which == 0 ? (LAYOUT == kGrouped ? 1.f / kPScale : 1.f) : sh.scale;
-  #pragma unroll
+          const float mul = which == 0 ? 1.f : sh.scale;
+#pragma unroll
           for (int cc = 0; cc < D / 64; ++cc) {
             const int c = h * (D / 64) + cc;  // 32-column chunk index
             uint32_t v[32];
             tmem_ld32(tacc + c * 32, v);
             tmem_wait_ld();
-  #pragma unroll
+#pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint4 x;
               x.x = pack_bf16x2(__uint_as_float(v[8 * u + 0]) * mul, __uint_as_float(v[8 * u + 1]) * mul);
@@ -1114,11 +1113,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           if (!ok) break;
           uint16_t* out = static_cast<uint16_t*>(which == 0 ? args.dv : args.dk);
           constexpr int G8 = D / 8;  // 16-byte units per row
-  #pragma unroll
+#pragma unroll
           for (int e = ktid; e < C::BN * G8; e += 256) {
             const int row = e / G8, g = e % G8;
             const int key_r = wk.key0 + row;
-            if (packed ? key_r < wk.sv.Lk : key_r < N)
+            if (key_r < N)
               *reinterpret_cast<uint4*>(out + k_row<LAYOUT>(args.pk, sh, wk.sv, wk.bh, key_r) * D + g * 8) =
                   *reinterpret_cast<const uint4*>(srow(row, g));
           }
@@ -1341,7 +1340,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           x[0] += lo4.x, x[1] += lo4.y, x[2] += lo4.z, x[3] += lo4.w;
           x[4] += hi4.x, x[5] += hi4.y, x[6] += hi4.z, x[7] += hi4.w;
         }
-        const float mul = which == 0 ? (LAYOUT == kGrouped ? 1.f / kPScale : 1.f) : sh.scale;
+        const float mul = which == 0 ? 1.f / kPScale : sh.scale;
         const int key = wk.key0 + row;
         if (key < wk.sv.Lk) {
           uint4 y;
