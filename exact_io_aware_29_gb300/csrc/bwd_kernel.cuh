@@ -368,10 +368,11 @@ __device__ __forceinline__ BwdWork bwd_work(const BwdArgs& args, int item) {
   return w;
 }
 
-// Packed layout, the 256 key-row threads (the grouped one: warp 15). The last
-// query and key blocks of a sequence also hold rows of the next one, which may
-// hold anything: a NaN there times the zero that P and dS have for those rows
-// would be a NaN in dK, dV and dQ. They are zeroed in shared memory once S^T has
+// Fixed and packed layouts, the 256 key-row threads (the grouped one: warp 15).
+// The last query and key blocks of a packed sequence also hold rows of the next
+// one, the last key block before a kv_lens also padding, and both may hold
+// anything: a NaN there times the zero that P and dS have for those rows would
+// be a NaN in dK, dV and dQ. They are zeroed in shared memory once S^T has
 // been read out of Q and K and nothing has read dO or V yet: rows of Q (its
 // slot) and dO from q_rows on, of K and V (in either buffer) from k_rows on.
 // False if a wait gave up. Out of line, so that it takes none of the loop's
@@ -962,6 +963,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         // S^T reads them: dV and dP^T, then dK and dQ, follow p_ready.
         if (LAYOUT == kPacked && ((qb + 1) * C::BM > wk.sv.Lq || (it == 0 && wk.key0 + C::BN > wk.sv.Lk))) {
           ok = bwd_clean_tiles<D>(smem, slot, wk.sv.Lq - qb * C::BM, it == 0 ? wk.sv.Lk - wk.key0 : C::BN, p & 1, ci & 1);
+          if (!ok) break;
+        }
+        // Fixed layout: keys past the batch entry's key length (TMA itself fills
+        // with zeros past N).
+        if (LAYOUT == kFixed && it == 0 && wk.sv.Lk < min(N, wk.key0 + C::BN)) {
+          ok = bwd_clean_tiles<D>(smem, slot, C::BM, wk.sv.Lk - wk.key0, p & 1, ci & 1);
           if (!ok) break;
         }
         tmem_wait_st();
