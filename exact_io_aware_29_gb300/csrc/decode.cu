@@ -132,8 +132,14 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (t / C::STAGES) & 1, abort_flag));
       if (!ok) break;
       const uint8_t* Kt = smem + s * C::STAGE_BYTES + box * C::BOX_BYTES;
-      const uint8_t* Vt = Kt + C::TILE_BYTES;
+      uint8_t* Vt = smem + s * C::STAGE_BYTES + box * C::BOX_BYTES + C::TILE_BYTES;
       const int kbase = c0 + t * C::TK;
+      if (kbase + C::TK > c1) {
+        // The last tile's slots past the last key may hold anything, and 0 * NaN
+        // is NaN: each thread zeroes what it will read (no copy follows here).
+        for (int r = grp; r < C::TK; r += C::GROUPS)
+          if (kbase + r >= c1) *reinterpret_cast<uint4*>(Vt + r * 128 + ((ch ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+      }
       float sc[C::KPG];
 #pragma unroll
       for (int i = 0; i < C::KPG; ++i) {
@@ -172,6 +178,12 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
           }
         }
         m = mx;
+      } else {
+        // No finite logit yet: NaN ones, which the maximum passes over, make
+        // the sum NaN (beside a finite maximum they do so by themselves).
+#pragma unroll
+        for (int i = 0; i < C::KPG; ++i)
+          if (sc[i] != sc[i]) l = sc[i];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
@@ -193,19 +205,16 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
       float M = -INFINITY;
       for (int g = 0; g < C::GROUPS; ++g) M = fmaxf(M, red_ml[2 * g]);
       float lsum = 0.f, acc = 0.f;
-      if (M > -INFINITY) {
-        for (int g = 0; g < C::GROUPS; ++g) {
-          const float mg = red_ml[2 * g];
-          if (mg == -INFINITY) continue;
-          const float f = ex2(mg - M);
-          lsum = fmaf(red_ml[2 * g + 1], f, lsum);
-          acc = fmaf(red_o[g * D + tid], f, acc);
-        }
+      for (int g = 0; g < C::GROUPS; ++g) {
+        if (red_ml[2 * g + 1] == 0.f) continue;  // no keys
+        const float f = ex2(red_ml[2 * g] - M);
+        lsum = fmaf(red_ml[2 * g + 1], f, lsum);
+        acc = fmaf(red_o[g * D + tid], f, acc);
       }
       if (nsplit_b == 1) {
-        const float outv = lsum > 0.f ? acc / lsum : 0.f;
+        const float outv = lsum == 0.f ? 0.f : acc / lsum;  // 0 and -inf for no keys only
         static_cast<__nv_bfloat16*>(a.o)[static_cast<size_t>(bh) * D + tid] = __float2bfloat16_rn(outv);
-        if (tid == 0) a.lse[bh] = lsum > 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+        if (tid == 0) a.lse[bh] = lsum == 0.f ? -INFINITY : (M + log2f(lsum)) * kLn2;
       } else {
         const size_t p = static_cast<size_t>(bh) * a.nsplit + split;
         a.part_o[p * D + tid] = acc;
@@ -231,18 +240,15 @@ __global__ void __launch_bounds__(D) fa_decode_combine_kernel(const DecodeArgs a
   float M = -INFINITY;
   for (int s = 0; s < ns; ++s) M = fmaxf(M, a.part_ml[2 * (p0 + s)]);
   float lsum = 0.f, acc = 0.f;
-  if (M > -INFINITY) {
-    for (int s = 0; s < ns; ++s) {
-      const float ms = a.part_ml[2 * (p0 + s)];
-      if (ms == -INFINITY) continue;
-      const float f = ex2(ms - M);
-      lsum = fmaf(a.part_ml[2 * (p0 + s) + 1], f, lsum);
-      acc = fmaf(a.part_o[(p0 + s) * D + threadIdx.x], f, acc);
-    }
+  for (int s = 0; s < ns; ++s) {
+    if (a.part_ml[2 * (p0 + s) + 1] == 0.f) continue;  // no keys
+    const float f = ex2(a.part_ml[2 * (p0 + s)] - M);
+    lsum = fmaf(a.part_ml[2 * (p0 + s) + 1], f, lsum);
+    acc = fmaf(a.part_o[(p0 + s) * D + threadIdx.x], f, acc);
   }
   static_cast<__nv_bfloat16*>(a.o)[static_cast<size_t>(bh) * D + threadIdx.x] =
-      __float2bfloat16_rn(lsum > 0.f ? acc / lsum : 0.f);
-  if (threadIdx.x == 0) a.lse[bh] = lsum > 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+      __float2bfloat16_rn(lsum == 0.f ? 0.f : acc / lsum);
+  if (threadIdx.x == 0) a.lse[bh] = lsum == 0.f ? -INFINITY : (M + log2f(lsum)) * kLn2;
 }
 
 template <int D>

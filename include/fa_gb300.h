@@ -223,6 +223,8 @@ int fa_bwd_varlen_gqa_deterministic(const void* q, const void* k, const void* v,
  *   q, o           device bf16 [B, H, d].
  *   k_cache, v_cache  device bf16 [num_blocks, block_size, H, d] (the pool).
  *   lse            device fp32 [B, H]; -inf and O = 0 for a sequence with no keys.
+ *                  (A NaN logit gives NaN in both. Slots past seq_lens[b] may
+ *                  hold anything.)
  *   block_table    device int32 [B, max_blocks_per_seq]; entries past a
  *                  sequence's last page are not read.
  *   seq_lens       device int32 [B], each in [0, max_seq_len].
