@@ -151,6 +151,9 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdArgs a, int Np
   }
   if (tid == 0) *a.ticket = 0u;  // (thread 0 of a block without a tile too)
   if (LAYOUT == kGrouped && !in_range) return;
+  // delta from the stored O: its bf16 rounding enters dS as P times 2^-8 of the
+  // row's |dO||O| terms, beside dS's own 2^-8 of P |dP - delta|; the forward keeps
+  // no O in 32 bits.
   uint4 o4[PASSES], d4[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
@@ -1007,6 +1010,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 const uint64_t pp = f2_pack(__uint_as_float(pk[c][q] << 16), __uint_as_float(pk[c][q] & 0xFFFF0000u));
                 f2_unpack(f2_mul(pp, f2_sub(dd, dlt[e])), da, db);
               }
+              // bf16: the type of K and Q, which the products with dS read (for
+              // f16 both would have to be converted, with a second pass for values
+              // outside its range, as the forward has for V). The largest rounding
+              // of dQ and dK beside the output's own: 2^-8 of each term.
               w[q] = pack_bf16x2(da, db);
             }
           }

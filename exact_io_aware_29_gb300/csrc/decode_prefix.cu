@@ -5,7 +5,10 @@
 // CTA covers one range of the keys for up to 256 rows, so that the prefix is
 // read once per 256 rows instead of once per sequence. Each row's partial O
 // (fp32, normalised) and log-sum go to the step's workspace and are joined
-// with the sequence's own part by the step's last kernel.
+// with the sequence's own part by the step's last kernel. P goes to the product
+// with V as f16 (2^-11 of each term; the streamed parts' hi + lo bf16 would be
+// two products on the pipe that bounds this one): 8 times finer than the
+// output's own rounding.
 #include "fwd_kernel.cuh"
 
 namespace fa {
