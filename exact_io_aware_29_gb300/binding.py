@@ -52,6 +52,11 @@ SIGNATURES = {
     "fa_qk_norm_rope_bwd": (_I, [_P] * 13 + [_I] * 6 + [_L] * 4 + [_F, _I, _P, ctypes.c_size_t, _P]),
     "fa_decode_shared_prefix_workspace_size": (ctypes.c_size_t, [_I] * 8),
     "fa_decode_shared_prefix": (_I, [_P] * 10 + [_I] * 12 + [_F, _P, ctypes.c_size_t, _P]),
+    "fa_kv_append": (_I, [_P] * 10 + [_I] * 8 + [_L, _L, _L, _I, _P]),
+    "fa_kv_append_q4": (_I, [_P] * 12 + [_I] * 8 + [_L, _L, _L, _I, _P]),
+    "fa_kv_gather_q4": (_I, [_P] * 9 + [_I] * 7 + [_P]),
+    "fa_decode_paged_q4_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "fa_decode_paged_q4": (_I, [_P] * 9 + [_I] * 9 + [_F, _P, ctypes.c_size_t, _P]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_last_cuda_error": (ctypes.c_char_p, []),
@@ -697,6 +702,223 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, dq_out,
     fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dwq, dwk, eps,
                         interleaved, workspace, stream)
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------------------
+# The paged cache: tokens appended to it, and the cache held in 4 bits.
+# ---------------------------------------------------------------------------
+def _check_append(where, q, k, v, cos, sin, positions, slots, q_out):
+    """Checks what both forms of the append take besides the cache: (device,
+    the C call's sizes up to max_pos, its token strides)."""
+    torch = _torch or _load_torch()
+    dev = _cuda_index(where, k)
+    ks = k.shape
+    if len(ks) != 3:
+        raise ValueError(f"{where}: k and v are [T, H_kv, d], q [T, H, d]; got {tuple(ks)}")
+    T, H_kv, d = ks
+    sk, sv = _heads_stride(where, "k", k, T, H_kv, d, dev), _heads_stride(where, "v", v, T, H_kv, d, dev)
+    H, sq = 0, 0
+    i32 = torch.int32
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{where}: q and q_out go together")
+    if q is not None:
+        if len(q.shape) != 3:
+            raise ValueError(f"{where}: q is [T, H, d]; got {tuple(q.shape)}")
+        H = q.shape[1]
+        sq = _heads_stride(where, "q", q, T, H, d, dev)
+        if q_out.dtype is not torch.bfloat16 or q_out.shape != (T, H, d) or not q_out.is_contiguous() \
+                or q_out.get_device() != dev:
+            _refuse(where, dev, (("q_out", q_out, torch.bfloat16, (T, H, d)),))
+    if slots.dtype is not i32 or slots.shape != (T,) or not slots.is_contiguous() or slots.get_device() != dev:
+        _refuse(where, dev, (("slots", slots, i32, (T,)),))
+    if cos is None and sin is None:
+        return dev, (T, H, H_kv, d, 0, 1), (sq, sk, sv)
+    if cos is None or sin is None or len(cos.shape) != 2:
+        raise ValueError(f"{where}: cos and sin are both [max_pos, rot / 2], or both None")
+    f32, table = torch.float32, cos.shape
+    if (cos.dtype is not f32 or not cos.is_contiguous() or cos.get_device() != dev
+            or sin.dtype is not f32 or sin.shape != table or not sin.is_contiguous() or sin.get_device() != dev):
+        _refuse(where, dev, (("cos", cos, f32, table), ("sin", sin, f32, table)))
+    if positions is None:
+        if table[1]:
+            raise ValueError(f"{where}: a rotation needs positions")
+    elif positions.dtype is not i32 or positions.shape != (T,) or not positions.is_contiguous() \
+            or positions.get_device() != dev:
+        _refuse(where, dev, (("positions", positions, i32, (T,)),))
+    return dev, (T, H, H_kv, d, 2 * table[1], table[0]), (sq, sk, sv)
+
+
+def fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, interleaved: bool = False,
+                 stream=None) -> None:
+    """New tokens rotated and written to a paged cache; same semantics as the
+    C entry point. q, k and v may be strided over tokens (parts of a fused
+    projection); the rotated width is 2 * cos.shape[1]. q and q_out may both
+    be None, and so may cos, sin and positions (no rotation)."""
+    where = "fa_kv_append"
+    dev, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
+    cs, bf16 = k_cache.shape, _torch.bfloat16
+    if len(cs) != 4 or cs[2:] != k.shape[1:]:
+        raise ValueError(f"{where}: the caches are [num_blocks, block_size, H_kv, d]; got {tuple(cs)}")
+    if (k_cache.dtype is not bf16 or not k_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.dtype is not bf16 or v_cache.shape != cs or not v_cache.is_contiguous()
+            or v_cache.get_device() != dev):
+        _refuse(where, dev, (("k_cache", k_cache, bf16, cs), ("v_cache", v_cache, bf16, cs)))
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_append, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(cos),
+                    _ptr(sin), _ptr(positions), slots.data_ptr(), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+                    *sizes, cs[0], cs[1], *strides, int(bool(interleaved)), _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, interleaved: bool = False, stream=None):
+    """Allocates the rotated queries [T, H, d], then calls fa_kv_append. Returns them."""
+    torch = _load_torch()
+    q_out = _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, interleaved, stream)
+    return q_out
+
+
+def _check_q4(where, dev, k_codes, k_scales, v_codes, v_scales, H_kv=None, d=None):
+    """Checks the four tensors of a 4-bit cache: (num_blocks, H_kv, block_size, d)."""
+    cs, u8, bf16 = k_codes.shape, _torch.uint8, _torch.bfloat16
+    if len(cs) != 4 or (d is not None and (cs[1] != H_kv or 2 * cs[3] != d)):
+        raise ValueError(f"{where}: the codes are [num_blocks, H_kv, block_size, d / 2]; got {tuple(cs)}")
+    ss = (cs[0], cs[1], cs[2], cs[3] // 32, 2)
+    if (k_codes.dtype is not u8 or not k_codes.is_contiguous() or k_codes.get_device() != dev
+            or v_codes.dtype is not u8 or v_codes.shape != cs or not v_codes.is_contiguous()
+            or v_codes.get_device() != dev
+            or k_scales.dtype is not bf16 or k_scales.shape != ss or not k_scales.is_contiguous()
+            or k_scales.get_device() != dev
+            or v_scales.dtype is not bf16 or v_scales.shape != ss or not v_scales.is_contiguous()
+            or v_scales.get_device() != dev):
+        _refuse(where, dev, (("k_codes", k_codes, u8, cs), ("v_codes", v_codes, u8, cs),
+                             ("k_scales", k_scales, bf16, ss), ("v_scales", v_scales, bf16, ss)))
+    return cs[0], cs[1], cs[2], 2 * cs[3]
+
+
+def kv_cache_q4(num_blocks: int, H_kv: int, block_size: int, d: int, device="cuda"):
+    """An empty 4-bit cache: (k_codes, k_scales, v_codes, v_scales), all zero."""
+    torch = _load_torch()
+    shape = (num_blocks, H_kv, block_size)
+    return tuple(t for _ in range(2) for t in (
+        torch.zeros(*shape, d // 2, dtype=torch.uint8, device=device),
+        torch.zeros(*shape, d // 64, 2, dtype=torch.bfloat16, device=device)))
+
+
+def fa_kv_append_q4(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scales, v_codes, v_scales,
+                    interleaved: bool = False, stream=None) -> None:
+    """fa_kv_append for a cache held in 4 bits; same semantics as the C entry point."""
+    where = "fa_kv_append_q4"
+    dev, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
+    num_blocks, _, block_size, _ = _check_q4(where, dev, k_codes, k_scales, v_codes, v_scales, sizes[2], sizes[3])
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_append_q4, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(cos),
+                    _ptr(sin), _ptr(positions), slots.data_ptr(), _ptr(q_out), k_codes.data_ptr(),
+                    k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *sizes, num_blocks, block_size,
+                    *strides, int(bool(interleaved)), _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def kv_append_q4(q, k, v, cos, sin, positions, slots, k_codes, k_scales, v_codes, v_scales,
+                 interleaved: bool = False, stream=None):
+    """Allocates the rotated queries [T, H, d], then calls fa_kv_append_q4. Returns them."""
+    torch = _load_torch()
+    q_out = _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    fa_kv_append_q4(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scales, v_codes, v_scales, interleaved,
+                    stream)
+    return q_out
+
+
+def fa_kv_gather_q4(k_codes, k_scales, v_codes, v_scales, block_table, starts, cu_seqlens_k, k, v,
+                    stream=None) -> None:
+    """Tokens of a 4-bit cache back as packed bf16 keys and values; same
+    semantics as the C entry point. starts may be None (token 0)."""
+    torch = _torch or _load_torch()
+    where = "fa_kv_gather_q4"
+    dev = _cuda_index(where, k_codes)
+    num_blocks, H_kv, block_size, d = _check_q4(where, dev, k_codes, k_scales, v_codes, v_scales)
+    ks, bf16, i32 = k.shape, torch.bfloat16, torch.int32
+    if len(ks) != 3 or ks[1] != H_kv or ks[2] != d or block_table.dim() != 2:
+        raise ValueError(f"{where}: k and v are [total_k, {H_kv}, {d}], the table [batch, blocks per sequence]; got "
+                         f"{tuple(ks)} and {tuple(block_table.shape)}")
+    batch, width = block_table.shape
+    if (k.dtype is not bf16 or not k.is_contiguous() or k.get_device() != dev
+            or v.dtype is not bf16 or v.shape != ks or not v.is_contiguous() or v.get_device() != dev
+            or block_table.dtype is not i32 or not block_table.is_contiguous() or block_table.get_device() != dev
+            or cu_seqlens_k.dtype is not i32 or cu_seqlens_k.shape != (batch + 1,)
+            or not cu_seqlens_k.is_contiguous() or cu_seqlens_k.get_device() != dev):
+        _refuse(where, dev, (("k", k, bf16, ks), ("v", v, bf16, ks), ("block_table", block_table, i32, (batch, width)),
+                             ("cu_seqlens_k", cu_seqlens_k, i32, (batch + 1,))))
+    if starts is not None and (starts.dtype is not i32 or starts.shape != (batch,) or not starts.is_contiguous()
+                               or starts.get_device() != dev):
+        _refuse(where, dev, (("starts", starts, i32, (batch,)),))
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_gather_q4, k_codes.data_ptr(), k_scales.data_ptr(),
+                    v_codes.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), _ptr(starts),
+                    cu_seqlens_k.data_ptr(), k.data_ptr(), v.data_ptr(), batch, H_kv, d, ks[0], num_blocks, block_size,
+                    width, _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def kv_gather_q4(k_codes, k_scales, v_codes, v_scales, block_table, starts, cu_seqlens_k, total_k: int, stream=None):
+    """Allocates K and V [total_k, H_kv, d], then calls fa_kv_gather_q4. Returns (K, V)."""
+    torch = _load_torch()
+    shape = (total_k, k_codes.shape[1], 2 * k_codes.shape[3])
+    k, v = _alloc(stream, lambda: [torch.empty(shape, dtype=torch.bfloat16, device=k_codes.device) for _ in range(2)])
+    fa_kv_gather_q4(k_codes, k_scales, v_codes, v_scales, block_table, starts, cu_seqlens_k, k, v, stream)
+    return k, v
+
+
+def fa_decode_paged_q4_workspace_size(B: int, n_new: int, H: int, H_kv: int, d: int, max_seq_len: int) -> int:
+    return int(load_library().fa_decode_paged_q4_workspace_size(B, n_new, H, H_kv, d, max_seq_len))
+
+
+def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seq_lens, max_seq_len: int,
+                       scale: float, workspace=None, stream=None) -> None:
+    """Decoding steps over a 4-bit paged cache with grouped heads; same
+    semantics as the C entry point. q and o are [B, n_new, H, d] with lse
+    [B, n_new, H], or [B, H, d] and [B, H] for one new query."""
+    torch = _torch or _load_torch()
+    where = "fa_decode_paged_q4"
+    dev = _cuda_index(where, q)
+    qs, bf16, i32 = q.shape, torch.bfloat16, torch.int32
+    if len(qs) not in (3, 4) or block_table.dim() != 2:
+        raise ValueError(f"{where}: q is [B, n_new, H, d] or [B, H, d], the table [B, blocks per sequence]; got "
+                         f"{tuple(qs)} and {tuple(block_table.shape)}")
+    num_blocks, H_kv, block_size, d = _check_q4(where, dev, k_codes, k_scales, v_codes, v_scales, k_codes.shape[1],
+                                                qs[-1])
+    B, H = qs[0], qs[-2]
+    rows, width = block_table.shape
+    if (q.dtype is not bf16 or not q.is_contiguous() or rows != B
+            or o.dtype is not bf16 or o.shape != qs or not o.is_contiguous() or o.get_device() != dev
+            or lse.dtype is not torch.float32 or lse.shape != qs[:-1] or not lse.is_contiguous()
+            or lse.get_device() != dev
+            or block_table.dtype is not i32 or not block_table.is_contiguous() or block_table.get_device() != dev
+            or seq_lens.dtype is not i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous()
+            or seq_lens.get_device() != dev):
+        _refuse(where, dev, (("q", q, bf16, qs), ("o", o, bf16, qs), ("lse", lse, torch.float32, qs[:-1]),
+                             ("block_table", block_table, i32, (B, width)), ("seq_lens", seq_lens, i32, (B,))))
+    n_new, max_seq_len = qs[1] if len(qs) == 4 else 1, int(max_seq_len)
+    workspace = _workspace(where, workspace, dev, stream, fa_decode_paged_q4_workspace_size, B, n_new, H, H_kv, d,
+                           max_seq_len)
+    st = _on_device(dev, (_LIB or load_library()).fa_decode_paged_q4, q.data_ptr(), k_codes.data_ptr(),
+                    k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                    block_table.data_ptr(), seq_lens.data_ptr(), B, n_new, H, H_kv, d, num_blocks, block_size, width,
+                    max_seq_len, float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                    _raw_stream(where, dev, stream))
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def attention_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, max_seq_len, scale,
+                              workspace=None, stream=None):
+    """Allocates O and LSE, then calls fa_decode_paged_q4. Returns (O, LSE)."""
+    torch = _load_torch()
+    o, lse = _alloc(stream, lambda: (torch.empty_like(q),
+                                     torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)))
+    fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seq_lens, max_seq_len, scale,
+                       workspace, stream)
+    return o, lse
 
 
 def fa_quantize_fp8(x, out, block_scale, transpose: bool, stream=None) -> None:

@@ -325,6 +325,57 @@ int check_shared_tables(const fa::SharedArgs& a, cudaStream_t stream) {
                              stream);
 }
 
+// How a step over a 4-bit cache splits its rows and keys over CTAs, from the
+// shapes alone: blocks of 8 rows, or 16 where there are more, and chunks of
+// whole 128-key tiles.
+void q4_plan(fa::Q4DecodeArgs* a) {
+  const int rows = a->n_new * (a->H / a->Hk);
+  a->rows_per = rows <= 8 ? 8 : 16;
+  a->row_blocks = (rows + a->rows_per - 1) / a->rows_per;
+  const long long base = static_cast<long long>(a->B) * a->Hk * a->row_blocks;
+  const long long tiles = (static_cast<long long>(a->max_seq_len) + 127) / 128;
+  const long long ns = std::min(std::max<long long>(912 / base, 1), tiles);
+  const long long per = (tiles + ns - 1) / ns;
+  a->chunk = static_cast<int>(per * 128);
+  a->nsplit = static_cast<int>((tiles + per - 1) / per);
+}
+
+// Check mode: the slots of an append are the pool's or negative, and no two alike.
+int check_slots(const int* slots, int T, long long pool, cudaStream_t stream) {
+  if (!check_mode()) return FA_OK;
+  std::vector<int> h(T);
+  cudaError_t e = cudaMemcpyAsync(h.data(), slots, sizeof(int) * T, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return launch_error(e);
+  std::sort(h.begin(), h.end());
+  for (int i = 0; i < T; ++i)
+    if (h[i] >= pool || (i > 0 && h[i] >= 0 && h[i] == h[i - 1])) return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+// Check mode: the tokens that a gather reads lie in blocks of the pool.
+int check_gather_tables(const int* table, const int* starts, const int* cu, int batch, int max_blocks, int block_size,
+                        int num_blocks, cudaStream_t stream) {
+  if (!check_mode()) return FA_OK;
+  std::vector<int> tab(static_cast<size_t>(batch) * max_blocks), first(batch, 0), at(batch + 1);
+  cudaError_t e = cudaMemcpyAsync(tab.data(), table, sizeof(int) * tab.size(), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess && starts != nullptr)
+    e = cudaMemcpyAsync(first.data(), starts, sizeof(int) * batch, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(at.data(), cu, sizeof(int) * at.size(), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return launch_error(e);
+  for (int b = 0; b < batch; ++b) {
+    const long long end = static_cast<long long>(first[b]) + at[b + 1] - at[b];
+    if (first[b] < 0 || end > static_cast<long long>(max_blocks) * block_size) return FA_ERR_INVALID;
+    for (long long p = first[b] / block_size; p * block_size < end; ++p) {
+      const int x = tab[static_cast<size_t>(b) * max_blocks + p];
+      if (x < 0 || x >= num_blocks) return FA_ERR_INVALID;
+    }
+  }
+  return FA_OK;
+}
+
 // Test hooks, read from the environment on every call: FA_TEST_WAIT_LIMIT_NS
 // bounds each device wait (default 2 s), FA_TEST_DROP_LOADS=1 makes the TMA
 // producers issue no loads so that the dependent waits run out. Used by the
@@ -352,6 +403,7 @@ int apply_test_hooks(cudaStream_t stream) {
   if (e == cudaSuccess) e = fa::set_bwd_gqa_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_shared_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_prefix_test_hooks(limit, drop, stream);
+  if (e == cudaSuccess) e = fa::set_decode_q4_test_hooks(limit, drop, stream);
   if (e != cudaSuccess) return launch_error(e);
   applied_limit = limit;
   applied_drop = drop;
@@ -410,7 +462,8 @@ int fa_check_status(void* stream) {
   if (e != cudaSuccess) return launch_error(e);
   const int words[] = {fa::take_fwd_status(), fa::take_bwd_status(),     fa::take_decode_status(),
                        fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status(),
-                       fa::take_decode_shared_status(), fa::take_decode_prefix_status()};
+                       fa::take_decode_shared_status(), fa::take_decode_prefix_status(),
+                       fa::take_decode_q4_status()};
   bool late = false;
   for (int w : words) {
     if (w == FA_ERR_LAUNCH) return launch_error(cudaGetLastError());
@@ -1145,6 +1198,215 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, cons
   a.dk_stride = dk_stride;
   a.part = static_cast<float*>(workspace);
   cudaError_t e = fa::launch_norm_rope_bwd(a, s);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+// Checks and arguments that the two forms of the append share (k_scales and
+// v_scales: nullptr for the bf16 cache).
+static int kv_append(const void* q, const void* k, const void* v, const float* cos, const float* sin,
+                     const int* positions, const int* slots, void* q_out, void* k_cache, void* k_scales, void* v_cache,
+                     void* v_scales, int T, int H, int H_kv, int d, int rot, int max_pos, int num_blocks,
+                     int block_size, long long q_stride, long long k_stride, long long v_stride, int interleaved,
+                     void* stream) {
+  if (!k || !v || !slots || !k_cache || !v_cache || (q == nullptr) != (q_out == nullptr)) return FA_ERR_INVALID;
+  if (rot < 0 || rot > d || (rot != 0 && (!cos || !sin || !positions || max_pos < 1))) return FA_ERR_INVALID;
+  if (num_blocks < 1 || block_size < 1 || H_kv < 1 || (q != nullptr && H < 1)) return FA_ERR_INVALID;
+  int st = check_shape(T, H_kv, 1, d, 1.f);
+  if (st == FA_OK && q != nullptr) st = check_shape(T, H, 1, d, 1.f);
+  if (st != FA_OK) return st;
+  const long long kv = static_cast<long long>(H_kv) * d;
+  if (k_stride < kv || v_stride < kv || (q != nullptr && q_stride < static_cast<long long>(H) * d))
+    return FA_ERR_INVALID;
+  if (rot % 16 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || (q != nullptr && q_stride % 8 != 0))
+    return FA_ERR_UNSUPPORTED;
+  const long long far = (1LL << 40) / T;
+  if (k_stride > far || v_stride > far || (q != nullptr && q_stride > far)) return FA_ERR_UNSUPPORTED;
+  const long long pool = static_cast<long long>(num_blocks) * block_size;
+  if (pool > 0x7fffffffLL || pool * kv > (1LL << 40) || (k_scales != nullptr && block_size % 16 != 0))
+    return FA_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k, v, q_out, k_cache, k_scales, v_cache, v_scales};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  if (rot != 0 && (!aligned16(cos) || !aligned16(sin))) return FA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rot != 0) st = check_positions(positions, T, max_pos, s);
+  if (st == FA_OK) st = check_slots(slots, T, pool, s);
+  if (st != FA_OK) return st;
+  fa::KvAppendArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.k_scales = k_scales;
+  a.v_cache = v_cache;
+  a.v_scales = v_scales;
+  a.T = T;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.H = q == nullptr ? 0 : H;
+  a.Hk = H_kv;
+  a.D = d;
+  a.rot = rot;
+  a.max_pos = max_pos;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.interleaved = interleaved ? 1 : 0;
+  cudaError_t e = fa::launch_kv_append(a, s);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+int fa_kv_append(const void* q, const void* k, const void* v, const float* cos, const float* sin,
+                 const int* positions, const int* slots, void* q_out, void* k_cache, void* v_cache, int T, int H,
+                 int H_kv, int d, int rot, int max_pos, int num_blocks, int block_size, long long q_stride,
+                 long long k_stride, long long v_stride, int interleaved, void* stream) {
+  return kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, nullptr, v_cache, nullptr, T, H, H_kv, d, rot,
+                   max_pos, num_blocks, block_size, q_stride, k_stride, v_stride, interleaved, stream);
+}
+
+int fa_kv_append_q4(const void* q, const void* k, const void* v, const float* cos, const float* sin,
+                    const int* positions, const int* slots, void* q_out, void* k_codes, void* k_scales, void* v_codes,
+                    void* v_scales, int T, int H, int H_kv, int d, int rot, int max_pos, int num_blocks,
+                    int block_size, long long q_stride, long long k_stride, long long v_stride, int interleaved,
+                    void* stream) {
+  if (!k_scales || !v_scales) return FA_ERR_INVALID;
+  return kv_append(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scales, v_codes, v_scales, T, H, H_kv, d,
+                   rot, max_pos, num_blocks, block_size, q_stride, k_stride, v_stride, interleaved, stream);
+}
+
+// The sizes of a 4-bit cache and its block tables.
+static int check_q4_cache(int H_kv, int d, int num_blocks, int block_size, int max_blocks) {
+  if (num_blocks < 1 || block_size < 1 || max_blocks < 1 || H_kv < 1) return FA_ERR_INVALID;
+  const long long pool = static_cast<long long>(num_blocks) * block_size;
+  if (block_size % 16 != 0 || pool > 0x7fffffffLL || pool * H_kv * d > (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                    const int* block_table, const int* starts, const int* cu_seqlens_k, void* k, void* v, int batch,
+                    int H_kv, int d, int total_k, int num_blocks, int block_size, int max_blocks_per_seq,
+                    void* stream) {
+  if (!k_codes || !k_scales || !v_codes || !v_scales || !block_table || !cu_seqlens_k || !k || !v)
+    return FA_ERR_INVALID;
+  if (batch < 1) return FA_ERR_INVALID;
+  int st = check_shape(total_k, H_kv, 1, d, 1.f);
+  if (st == FA_OK) st = check_q4_cache(H_kv, d, num_blocks, block_size, max_blocks_per_seq);
+  if (st != FA_OK) return st;
+  const void* ptrs[] = {k_codes, k_scales, v_codes, v_scales, k, v};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_cu_seqlens(cu_seqlens_k, batch, total_k, total_k, s, true);
+  if (st == FA_OK)
+    st = check_gather_tables(block_table, starts, cu_seqlens_k, batch, max_blocks_per_seq, block_size, num_blocks, s);
+  if (st != FA_OK) return st;
+  fa::KvGatherArgs a{};
+  a.k_codes = k_codes;
+  a.k_scales = k_scales;
+  a.v_codes = v_codes;
+  a.v_scales = v_scales;
+  a.block_table = block_table;
+  a.starts = starts;
+  a.cu = cu_seqlens_k;
+  a.k = k;
+  a.v = v;
+  a.batch = batch;
+  a.Hk = H_kv;
+  a.D = d;
+  a.total = total_k;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.max_blocks = max_blocks_per_seq;
+  cudaError_t e = fa::launch_kv_gather_q4(a, s);
+  if (e != cudaSuccess) return launch_error(e);
+  if (check_mode()) return fa_check_status(stream);
+  return FA_OK;
+}
+
+// Sizes of a step over a 4-bit cache, checked, and its plan.
+static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int d, int max_seq_len, float scale) {
+  if (n_new < 1 || H < 1 || H_kv < 1 || H % H_kv != 0) return FA_ERR_INVALID;
+  int st = check_shape(B, H, max_seq_len, d, scale);
+  if (st == FA_OK) st = check_shape(B, H, n_new, d, scale);
+  if (st != FA_OK) return st;
+  const long long rows = static_cast<long long>(n_new) * (H / H_kv);
+  if (rows * B * H_kv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  *a = fa::Q4DecodeArgs{};
+  a->B = B;
+  a->n_new = n_new;
+  a->H = H;
+  a->Hk = H_kv;
+  a->D = d;
+  a->max_seq_len = max_seq_len;
+  a->scale_log2 = scale * fa::kLog2e;
+  q4_plan(a);
+  return FA_OK;
+}
+
+// Bytes of the partial O, then of the partial sums, of a plan.
+static size_t q4_part_bytes(const fa::Q4DecodeArgs& a, size_t* o_bytes) {
+  const size_t parts = static_cast<size_t>(a.B) * a.n_new * a.H * a.nsplit;
+  *o_bytes = align_up(parts * a.D * 4, 256);
+  return *o_bytes + align_up(parts * 4, 256);
+}
+
+size_t fa_decode_paged_q4_workspace_size(int B, int n_new, int H, int H_kv, int d, int max_seq_len) {
+  fa::Q4DecodeArgs a;
+  if (q4_sizes(&a, B, n_new, H, H_kv, d, max_seq_len, 1.f) != FA_OK) return 0;
+  size_t o_bytes;
+  return q4_part_bytes(a, &o_bytes);
+}
+
+int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                       const void* v_scales, void* o, float* lse, const int* block_table, const int* seq_lens, int B,
+                       int n_new, int H, int H_kv, int d, int num_blocks, int block_size, int max_blocks_per_seq,
+                       int max_seq_len, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !o || !lse || !block_table || !seq_lens)
+    return FA_ERR_INVALID;
+  fa::Q4DecodeArgs a;
+  int st = q4_sizes(&a, B, n_new, H, H_kv, d, max_seq_len, scale);
+  if (st == FA_OK) st = check_q4_cache(H_kv, d, num_blocks, block_size, max_blocks_per_seq);
+  if (st != FA_OK) return st;
+  if (static_cast<long long>(max_seq_len) > static_cast<long long>(max_blocks_per_seq) * block_size)
+    return FA_ERR_INVALID;
+  const void* ptrs[] = {q, k_codes, k_scales, v_codes, v_scales, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
+  size_t o_bytes;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < q4_part_bytes(a, &o_bytes))
+    return FA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = check_decode_tables(seq_lens, block_table, B, max_blocks_per_seq, block_size, num_blocks, max_seq_len, s);
+  if (st != FA_OK) return st;
+  st = apply_test_hooks(s);
+  if (st != FA_OK) return st;
+  a.q = q;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.k_scales = static_cast<const uint8_t*>(k_scales);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.v_scales = static_cast<const uint8_t*>(v_scales);
+  a.o = o;
+  a.lse = lse;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.piece = std::min(block_size & -block_size, 128);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
+  fa::LaunchMarks marks;
+  const bool timed = next_marks(&marks, 4, 2);
+  cudaError_t e = fa::launch_decode_q4(a, s, timed ? &marks : nullptr);
   if (e != cudaSuccess) return launch_error(e);
   if (check_mode()) return fa_check_status(stream);
   return FA_OK;

@@ -251,6 +251,55 @@ constexpr int kNormRopeMaxCtas = 152 * 2;  // of the backward: one row of partia
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, cudaStream_t stream);
 
+// Tokens appended to a paged cache (kv_cache.cu).
+struct KvAppendArgs {
+  const void *q, *k, *v;      // bf16 rows of d elements, heads side by side, tokens *_stride elements apart
+  const float *cos, *sin;     // fp32 [max_pos, rot / 2]
+  const int* positions;       // int32 [T], clamped to [0, max_pos)
+  const int* slots;           // int32 [T]: block * block_size + offset; others than the pool's are not written
+  void* q_out;                // bf16 [T, H, d]
+  void *k_cache, *v_cache;    // bf16 [num_blocks, block_size, Hk, d], or codes [num_blocks, Hk, block_size, d / 2]
+  void *k_scales, *v_scales;  // 4 bits: bf16 (s, z) [num_blocks, Hk, block_size, d / 64, 2]; nullptr for bf16
+  long long T, q_stride, k_stride, v_stride;
+  int H, Hk, D, rot, max_pos, num_blocks, block_size, interleaved;  // H = 0: no queries
+  int rows, q_slices, k_slices;  // set at launch: heads per unit of work, units per token
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+
+// Tokens of a 4-bit cache read back as packed bf16 (kv_cache.cu).
+struct KvGatherArgs {
+  const void *k_codes, *k_scales, *v_codes, *v_scales;  // the cache, as above
+  const int* block_table;     // int32 [batch, max_blocks]
+  const int* starts;          // int32 [batch]: first token of each sequence, or nullptr for 0
+  const int* cu;              // int32 [batch + 1]: packed rows of each sequence
+  void *k, *v;                // bf16 [total, Hk, d]
+  int batch, Hk, D, total, num_blocks, block_size, max_blocks;
+  int rows, slices;           // set at launch: heads per unit of work, units per row
+};
+cudaError_t launch_kv_gather_q4(const KvGatherArgs& a, cudaStream_t stream);
+
+// Decoding steps over a 4-bit cache (decode_q4.cu).
+struct Q4DecodeArgs {
+  const void* q;              // bf16 [B, n_new, H, D]
+  const uint8_t *k_codes, *v_codes;    // [num_blocks, Hk, block_size, D / 2]
+  const uint8_t *k_scales, *v_scales;  // bf16 (s, z) [num_blocks, Hk, block_size, D / 64, 2]
+  void* o;                    // bf16 [B, n_new, H, D]
+  float* lse;                 // fp32 [B, n_new, H], natural log
+  const int* block_table;     // int32 [B, max_blocks]
+  const int* seq_lens;        // int32 [B], clamped to [0, max_seq_len]
+  int B, n_new, H, Hk, D;
+  int block_size, num_blocks, max_blocks, max_seq_len;
+  int piece;                  // keys of one copy: a power of two from 16 on that divides the block size
+  int row_blocks, rows_per;   // blocks of rows_per rows (row = query * G + head) of each sequence and key head
+  int chunk, nsplit;          // keys per CTA and CTAs per (sequence, key head, row block)
+  float scale_log2;           // scale * log2(e)
+  float* part_o;              // workspace fp32 [B * n_new * H, nsplit, D], normalised (nsplit > 1)
+  float* part_lse;            // workspace fp32 [B * n_new * H, nsplit], base 2
+};
+cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks);
+cudaError_t set_decode_q4_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
+int take_decode_q4_status();
+
 // Sequences [first, first + n) behind prefix p of a shared-prefix step.
 __device__ __forceinline__ void prefix_seqs(const SharedArgs& a, int p, int& first, int& n) {
   first = min(max(a.cu_seqs[p], 0), a.B);

@@ -367,6 +367,109 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, cons
                         long long dk_stride, float eps, int interleaved, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/*
+ * Appending tokens to a paged KV cache, with the position rotation applied on
+ * the way: for token t, each pair (a, b) of the first `rot` elements of every
+ * head of its q and k is replaced by (a cos - b sin, b cos + a sin) (tables,
+ * pairs and `interleaved` as in fa_qk_norm_rope; every product and sum rounded
+ * to fp32, the result to bf16), q goes to q_out and the rotated k, and v as it
+ * is, to slot slots[t] of the cache: slot (p * block_size + i) is token i of
+ * block p. The cache is the one fa_decode_paged (H_kv = H) and
+ * fa_decode_shared_prefix read.
+ *   q, k, v        device bf16: element e of head h of token t at
+ *                  [t * stride + h * d + e] (strides in elements, multiples of
+ *                  8, >= heads * d), so all three can be parts of a fused
+ *                  projection. q and q_out may both be NULL (H and q_stride
+ *                  are then not looked at).
+ *   cos, sin       device fp32 [max_pos, rot / 2], 16-byte aligned;
+ *   positions      device int32 [T], in [0, max_pos) (check mode rejects others
+ *                  on the host; otherwise they are clamped on the device). With
+ *                  rot = 0 the three are not read and may be NULL.
+ *   slots          device int32 [T]. A token whose slot is not one of the pool's
+ *                  (a negative one marks padding) is not written; its q is
+ *                  rotated all the same. Two tokens must not have the same slot
+ *                  (what it holds then is not defined). Check mode rejects slots
+ *                  past the pool and slots that occur twice.
+ *   q_out          device bf16 [T, H, d], contiguous.
+ *   k_cache, v_cache  device bf16 [num_blocks, block_size, H_kv, d]; other slots
+ *                  are left as they were.
+ *   rot            a multiple of 16 in [0, d]; d in {64, 128}.
+ * Errors as for fa_qk_norm_rope; FA_ERR_UNSUPPORTED also for a pool of 2^31 or
+ * more slots.
+ */
+int fa_kv_append(const void* q, const void* k, const void* v, const float* cos, const float* sin,
+                 const int* positions, const int* slots, void* q_out, void* k_cache, void* v_cache, int T, int H,
+                 int H_kv, int d, int rot, int max_pos, int num_blocks, int block_size, long long q_stride,
+                 long long k_stride, long long v_stride, int interleaved, void* stream);
+
+/*
+ * The same for a cache held in 4 bits (4.5 with the scales): 64 consecutive
+ * elements x of a key or value row (as fa_kv_append would store it) become
+ *   z = min x,  s = bf16((max x - min x) / 15) (0 below 2^-126),
+ *   code = (x - z) / s to the nearest integer, ties to even, in 0..15 (0 if s = 0)
+ * and stand for z + s * code. A group with a NaN or an infinity, or whose range
+ * is past fp32, reads as NaN (s = z = NaN, codes 0).
+ *   k_codes, v_codes    device uint8 [num_blocks, H_kv, block_size, d / 2]: byte
+ *                       j holds element 2 j in its low half, 2 j + 1 in its high.
+ *   k_scales, v_scales  device bf16 [num_blocks, H_kv, block_size, d / 64, 2]: (s, z).
+ *   block_size          a multiple of 16 (FA_ERR_UNSUPPORTED otherwise).
+ */
+int fa_kv_append_q4(const void* q, const void* k, const void* v, const float* cos, const float* sin,
+                    const int* positions, const int* slots, void* q_out, void* k_codes, void* k_scales, void* v_codes,
+                    void* v_scales, int T, int H, int H_kv, int d, int rot, int max_pos, int num_blocks,
+                    int block_size, long long q_stride, long long k_stride, long long v_stride, int interleaved,
+                    void* stream);
+
+/*
+ * Tokens of that cache back as packed keys and values, for prompts continued
+ * behind it (fa_fwd_varlen_gqa): rows cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1 of
+ * k and v become tokens starts[b], starts[b] + 1, ... of sequence b, each
+ * z + s * code rounded to bf16.
+ *   block_table    device int32 [batch, max_blocks_per_seq] (entries of pages
+ *                  that hold none of the tokens are not read).
+ *   starts         device int32 [batch], or NULL for 0.
+ *   cu_seqlens_k   device int32 [batch + 1], non-decreasing, [0] = 0, [batch] <=
+ *                  total_k.
+ *   k, v           device bf16 [total_k, H_kv, d]. Rows of no sequence are left
+ *                  as they were.
+ * Check mode validates offsets, starts and tables on the host; otherwise tokens
+ * outside the table's row and blocks outside the pool read as zeros.
+ */
+int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                    const int* block_table, const int* starts, const int* cu_seqlens_k, void* k, void* v, int batch,
+                    int H_kv, int d, int total_k, int num_blocks, int block_size, int max_blocks_per_seq,
+                    void* stream);
+
+/*
+ * Decoding steps over that cache, with grouped heads (query head h reads key
+ * head h / (H / H_kv)): the n_new newest queries of each sequence, whose own
+ * keys and values are in the cache already, attend to its seq_lens[b] tokens,
+ * bottom-right causal: query i sees token c iff c <= seq_lens[b] - n_new + i. One
+ * generated token is n_new = 1; more are drafts looked over at once, or a short
+ * prompt behind a long context.
+ *   q, o           device bf16 [B, n_new, H, d];  lse  device fp32 [B, n_new, H]
+ *                  (natural log; -inf and O = 0 for a query that sees no token,
+ *                  and for nothing else: a NaN logit gives NaN in both).
+ *   block_table    device int32 [B, max_blocks_per_seq];  seq_lens device int32
+ *                  [B], each in [0, max_seq_len]. Entries past a sequence's last
+ *                  page are not read; slots past its length may hold anything.
+ *   block_size     a multiple of 16; max_seq_len <= max_blocks_per_seq * block_size.
+ *   workspace      >= fa_decode_paged_q4_workspace_size(...) bytes, 16-byte
+ *                  aligned, caller-owned. Calls that overlap on the GPU need
+ *                  workspaces of their own.
+ * Logits, softmax and sums are those of the cache's values z + s * code as they
+ * are, in fp32 (a row of q with elements of 2^114 or more may give NaN).
+ * Results are bitwise repeatable. Lengths and tables are checked on the host
+ * only in check mode (FA_CHECK=1); otherwise lengths are clamped to
+ * [0, max_seq_len] and block ids outside [0, num_blocks) read as zero keys and
+ * values. Errors as for fa_decode_paged.
+ */
+size_t fa_decode_paged_q4_workspace_size(int B, int n_new, int H, int H_kv, int d, int max_seq_len);
+int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                       const void* v_scales, void* o, float* lse, const int* block_table, const int* seq_lens, int B,
+                       int n_new, int H, int H_kv, int d, int num_blocks, int block_size, int max_blocks_per_seq,
+                       int max_seq_len, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the kernels' device status word:
  * FA_OK, FA_ERR_TIMEOUT, or FA_ERR_LAUNCH for a CUDA error. */
 int fa_check_status(void* stream);

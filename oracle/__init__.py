@@ -25,3 +25,11 @@ from .attention import (  # noqa: F401
 )
 from .norm_rope import norm_rope_backward, norm_rope_forward  # noqa: F401
 from .shared import shared_prefix_decode_forward  # noqa: F401
+from .kv_cache import (  # noqa: F401
+    held_q4,
+    q4_decode_forward,
+    quantise_q4,
+    rotated,
+    to_bf16,
+    unpack_codes,
+)
