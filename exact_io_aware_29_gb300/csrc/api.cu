@@ -325,21 +325,6 @@ int check_shared_tables(const fa::SharedArgs& a, cudaStream_t stream) {
                              stream);
 }
 
-// How a step over a 4-bit cache splits its rows and keys over CTAs, from the
-// shapes alone: blocks of 8 rows, or 16 where there are more, and chunks of
-// whole 128-key tiles.
-void q4_plan(fa::Q4DecodeArgs* a) {
-  const int rows = a->n_new * (a->H / a->Hk);
-  a->rows_per = rows <= 8 ? 8 : 16;
-  a->row_blocks = (rows + a->rows_per - 1) / a->rows_per;
-  const long long base = static_cast<long long>(a->B) * a->Hk * a->row_blocks;
-  const long long tiles = (static_cast<long long>(a->max_seq_len) + 127) / 128;
-  const long long ns = std::min(std::max<long long>(912 / base, 1), tiles);
-  const long long per = (tiles + ns - 1) / ns;
-  a->chunk = static_cast<int>(per * 128);
-  a->nsplit = static_cast<int>((tiles + per - 1) / per);
-}
-
 // Check mode: the slots of an append are the pool's or negative, and no two alike.
 int check_slots(const int* slots, int T, long long pool, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
@@ -1338,8 +1323,6 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   int st = check_shape(B, H, max_seq_len, d, scale);
   if (st == FA_OK) st = check_shape(B, H, n_new, d, scale);
   if (st != FA_OK) return st;
-  const long long rows = static_cast<long long>(n_new) * (H / H_kv);
-  if (rows * B * H_kv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   *a = fa::Q4DecodeArgs{};
   a->B = B;
   a->n_new = n_new;
@@ -1348,22 +1331,33 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   a->D = d;
   a->max_seq_len = max_seq_len;
   a->scale_log2 = scale * fa::kLog2e;
-  q4_plan(a);
+  const long long rows = static_cast<long long>(n_new) * (H / H_kv);
+  a->rows_per = rows <= 8 ? 8 : 16;
+  const long long blocks = (rows + a->rows_per - 1) / a->rows_per;
+  const long long tiles = (static_cast<long long>(max_seq_len) + fa::kQ4Tile - 1) / fa::kQ4Tile;
+  if (rows * B * H_kv > 0x7fffffffLL || tiles * B * H_kv > 0x7fffffffLL / blocks) return FA_ERR_UNSUPPORTED;
+  a->row_blocks = static_cast<int>(blocks);
+  a->most_tiles = static_cast<int>(tiles * B * H_kv * blocks);
   return FA_OK;
 }
 
-// Bytes of the partial O, then of the partial sums, of a plan.
-static size_t q4_part_bytes(const fa::Q4DecodeArgs& a, size_t* o_bytes) {
-  const size_t parts = static_cast<size_t>(a.B) * a.n_new * a.H * a.nsplit;
-  *o_bytes = align_up(parts * a.D * 4, 256);
-  return *o_bytes + align_up(parts * 4, 256);
+// Bytes of the partial O, the partial sums and the cuts.
+struct Q4Workspace {
+  size_t o, lse, cuts;
+};
+static Q4Workspace q4_workspace(const fa::Q4DecodeArgs& a) {
+  const size_t rows = static_cast<size_t>(2 * fa::kQ4MaxCtas) * a.rows_per;
+  return Q4Workspace{rows * a.D * 4, rows * 4, fa::kQ4MaxCtas * sizeof(int4)};
+}
+static size_t q4_workspace_bytes(const fa::Q4DecodeArgs& a) {
+  const Q4Workspace w = q4_workspace(a);
+  return w.o + w.lse + w.cuts;
 }
 
 size_t fa_decode_paged_q4_workspace_size(int B, int n_new, int H, int H_kv, int d, int max_seq_len) {
   fa::Q4DecodeArgs a;
   if (q4_sizes(&a, B, n_new, H, H_kv, d, max_seq_len, 1.f) != FA_OK) return 0;
-  size_t o_bytes;
-  return q4_part_bytes(a, &o_bytes);
+  return q4_workspace_bytes(a);
 }
 
 int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
@@ -1381,8 +1375,7 @@ int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
   const void* ptrs[] = {q, k_codes, k_scales, v_codes, v_scales, o};
   for (const void* p : ptrs)
     if (!aligned16(p)) return FA_ERR_UNSUPPORTED;
-  size_t o_bytes;
-  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < q4_part_bytes(a, &o_bytes))
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < q4_workspace_bytes(a))
     return FA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = check_decode_tables(seq_lens, block_table, B, max_blocks_per_seq, block_size, num_blocks, max_seq_len, s);
@@ -1401,9 +1394,11 @@ int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
   a.block_size = block_size;
   a.num_blocks = num_blocks;
   a.max_blocks = max_blocks_per_seq;
-  a.piece = std::min(block_size & -block_size, 128);
+  a.piece = std::min(block_size & -block_size, fa::kQ4Tile);
+  const Q4Workspace ws = q4_workspace(a);
   a.part_o = static_cast<float*>(workspace);
-  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.o);
+  a.cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.o + ws.lse);
   fa::LaunchMarks marks;
   const bool timed = next_marks(&marks, 4, 2);
   cudaError_t e = fa::launch_decode_q4(a, s, timed ? &marks : nullptr);

@@ -95,7 +95,7 @@ class Step:
         E = self.d * 2.0 ** -23 * M + 2.0 ** -22 + 2.0 ** -22 * M
         assert E < 0.05  # P within a fifth of itself at worst: a key left out, or one too many, still shows
         tol = 2.0 ** -8 * np.abs(ro) + 4 * E * ra + (143 * 2.0 ** -17 + 143 * 2.0 ** -23 * (L / 32 + 16)) * S
-        assert np.all(np.isfinite(go)) and np.all(np.abs(go - ro) <= tol)
+        assert bool(np.all(np.isfinite(go))) and float(np.max(np.abs(go - ro) - tol)) <= 0
         assert np.array_equal(np.isinf(gl), np.isinf(rl)) and not np.any(np.isnan(gl))
         fin = np.isfinite(rl)
         assert np.all(np.abs(gl - rl)[fin] <= E + 2.0 ** -24 * (L / 32 + 64) + 2.0 ** -22 * (1 + np.abs(rl[fin])))
