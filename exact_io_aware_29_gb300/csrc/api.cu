@@ -388,7 +388,6 @@ int apply_test_hooks(cudaStream_t stream) {
   if (e == cudaSuccess) e = fa::set_bwd_gqa_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_shared_test_hooks(limit, drop, stream);
   if (e == cudaSuccess) e = fa::set_decode_prefix_test_hooks(limit, drop, stream);
-  if (e == cudaSuccess) e = fa::set_decode_q4_test_hooks(limit, drop, stream);
   if (e != cudaSuccess) return launch_error(e);
   applied_limit = limit;
   applied_drop = drop;
@@ -447,8 +446,7 @@ int fa_check_status(void* stream) {
   if (e != cudaSuccess) return launch_error(e);
   const int words[] = {fa::take_fwd_status(), fa::take_bwd_status(),     fa::take_decode_status(),
                        fa::take_fp8_status(), fa::take_fwd_gqa_status(), fa::take_bwd_gqa_status(),
-                       fa::take_decode_shared_status(), fa::take_decode_prefix_status(),
-                       fa::take_decode_q4_status()};
+                       fa::take_decode_shared_status(), fa::take_decode_prefix_status()};
   bool late = false;
   for (int w : words) {
     if (w == FA_ERR_LAUNCH) return launch_error(cudaGetLastError());
@@ -1380,8 +1378,6 @@ int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = check_decode_tables(seq_lens, block_table, B, max_blocks_per_seq, block_size, num_blocks, max_seq_len, s);
   if (st != FA_OK) return st;
-  st = apply_test_hooks(s);
-  if (st != FA_OK) return st;
   a.q = q;
   a.k_codes = static_cast<const uint8_t*>(k_codes);
   a.k_scales = static_cast<const uint8_t*>(k_scales);
@@ -1394,7 +1390,6 @@ int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
   a.block_size = block_size;
   a.num_blocks = num_blocks;
   a.max_blocks = max_blocks_per_seq;
-  a.piece = std::min(block_size & -block_size, fa::kQ4Tile);
   const Q4Workspace ws = q4_workspace(a);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.o);

@@ -289,20 +289,17 @@ struct Q4DecodeArgs {
   const int* seq_lens;        // int32 [B], clamped to [0, max_seq_len]
   int B, n_new, H, Hk, D;
   int block_size, num_blocks, max_blocks, max_seq_len;
-  int piece;                  // keys of one copy: a power of two from 16 on that divides the block size
   int row_blocks, rows_per;   // blocks of rows_per rows (row = query * G + head) of each sequence and key head
-  int most_tiles;             // no more 128-key tiles in all than this
+  int most_tiles;             // no more tiles in all than this
   float scale_log2;           // scale * log2(e)
   // The workspace: two parts (its first and its last item) of every CTA, and the items that CTAs cut.
   float* part_o;              // fp32 [2 kQ4MaxCtas][rows_per][D], normalised
   float* part_lse;            // fp32 [2 kQ4MaxCtas][rows_per], base 2
   int4* cuts;                 // [kQ4MaxCtas]: (sequence or -1, item of it, part of the CTA before it, last CTA)
 };
-constexpr int kQ4Tile = 128;          // keys of a tile
-constexpr int kQ4MaxCtas = 4 * 152;   // four per SM
+constexpr int kQ4Tile = 128;           // keys of a tile
+constexpr int kQ4MaxCtas = 4 * 152;    // four per SM
 cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks);
-cudaError_t set_decode_q4_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream);
-int take_decode_q4_status();
 
 // Sequences [first, first + n) behind prefix p of a shared-prefix step.
 __device__ __forceinline__ void prefix_seqs(const SharedArgs& a, int p, int& first, int& n) {

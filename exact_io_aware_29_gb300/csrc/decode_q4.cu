@@ -26,9 +26,11 @@
 //
 // A persistent grid shares the 128-key tiles of all sequences and key heads out
 // evenly, in order, whatever their lengths: a CTA takes a run of tiles, whole
-// items (row block, key head) and the ends of two. One warp streams the tiles
-// through a ring with bulk copies (a block's keys of one head lie together:
-// codes, then scales, in up to 8 pieces), the others compute on 16 keys each.
+// items (row block, key head) and the ends of two. Each of its four warps works
+// on 32 keys of every tile (two independent halves hide each other's latencies),
+// which it copies ahead itself into a ring of its own (cp.async, 16 bytes a
+// lane; what is not there is filled with zeros), so that warps meet only where
+// an item ends.
 // Softmax statistics and sums are fp32. A cut item's parts are joined in the
 // order of the keys by a second kernel.
 #include <cuda_bf16.h>
@@ -40,24 +42,24 @@ namespace fa {
 
 template <int D, int NT>
 struct Q4Cfg {
-  static constexpr int TK = kQ4Tile;               // keys per tile
   static constexpr int NG = D / 64;                // groups of a row
   static constexpr int ROWS = 8 * NT;              // rows of an item
-  static constexpr int CODE_BYTES = TK * D / 2;
-  static constexpr int SCALE_BYTES = TK * NG * 4;
-  static constexpr int OFF_KS = CODE_BYTES, OFF_VC = OFF_KS + SCALE_BYTES, OFF_VS = OFF_VC + CODE_BYTES;
+  static constexpr int KEYS = 32;                  // a warp's keys of a tile
+  static constexpr int HALVES = KEYS / 16;
+  static constexpr int WARPS = kQ4Tile / KEYS;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NT - 1);  // per SM (registers: 168, 128 at d 64 with NT = 1)
+  // A stage of a warp's ring: codes of K and V, scales of K and V.
+  static constexpr int CODE_BYTES = KEYS * D / 2, SCALE_BYTES = KEYS * NG * 4;
+  static constexpr int OFF_VC = CODE_BYTES, OFF_KS = 2 * CODE_BYTES, OFF_VS = OFF_KS + SCALE_BYTES;
   static constexpr int STAGE_BYTES = 2 * (CODE_BYTES + SCALE_BYTES);
-  static constexpr int CWARPS = 4;                 // consumer warps
-  static constexpr int THREADS = (CWARPS + 1) * 32;
-  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NT - 1);  // per SM
-  static constexpr int STAGES = D == 64 ? 5 : 2 + NT;
+  static constexpr int STAGES = D == 64 ? 4 : 2 + NT;
   static constexpr int RED_STRIDE = D + 4;         // floats of a row in the join of the warps
-  static constexpr int OFF_RED = STAGES * STAGE_BYTES;
-  static constexpr int OFF_ML = OFF_RED + CWARPS * ROWS * RED_STRIDE * 4;
-  static constexpr int OFF_BAR = OFF_ML + CWARPS * ROWS * 2 * 4;
-  static constexpr int OFF_SCAN = OFF_BAR + 2 * STAGES * 8;
-  static constexpr int SMEM_BYTES = OFF_SCAN + STAGES * 4 + 4 + (CWARPS + 1) * 4 + 16;
-  static_assert(SMEM_BYTES * CTAS <= 227 * 1024 - (CTAS - 1) * 1024, "fits in an SM");
+  static constexpr int OFF_RED = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int OFF_ML = OFF_RED + WARPS * ROWS * RED_STRIDE * 4;
+  static constexpr int OFF_SCAN = OFF_ML + WARPS * ROWS * 2 * 4;
+  static constexpr int SMEM_BYTES = OFF_SCAN + WARPS * 4 + 8;
+  static_assert((SMEM_BYTES + 1024) * CTAS <= 228 * 1024, "fits in an SM");
 };
 
 namespace {
@@ -83,6 +85,17 @@ __device__ __forceinline__ int exponent(float x) { return static_cast<int>((__fl
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 16 bytes global -> shared, asynchronously; zeros if !on.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+// The larger of each pair of f16 (NaN only where both are).
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -226,39 +239,27 @@ __device__ __forceinline__ float column_max(float x) {
   return x;
 }
 
-// 16 keys of a tile from key k0 of it on. MASKED: some of them may be hidden
-// from some rows (row x sees the tile's keys below open + (row0 + x) / G - row0 / G),
-// or past the sequence (`left` keys of the tile are in it), or in a block that
-// is not in the pool (held = false: they read as zeros).
+// The keys of a stage. MASKED: some of them may be hidden from some rows (row x
+// sees the keys below open + (row0 + x) / G - row0 / G) or past the sequence
+// (`left` of them are in it).
 template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void q4_slice(const uint8_t* st, int k0, int lane, bool held, int left, int open, int row0,
-                                         int G, const Q4Rows<D, NT>& R, Q4State<D, NT>& S) {
+__device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, int open, int row0, int G,
+                                        const Q4Rows<D, NT>& R, Q4State<D, NT>& S) {
   using C = Q4Cfg<D, NT>;
-  constexpr int NG = D / 64;
+  constexpr int NG = D / 64, KH = 2 * C::HALVES;  // key ka + 8 h of a lane, h < KH
   const int r = lane >> 2, c = lane & 3;
   // Row i of the A operand of Q K^T, and k index i of P V, is key (i >> 1) + 4 (i & 1)
   // of its eight: the lanes of a load then meet two banks' worth of rows, not one.
-  const int ka = k0 + (r >> 1) + 4 * (r & 1);
-  float sc[NT][2][2];  // [key ka + 8 h][row i]
-  float vs[NG][2], vz[NG][2];
-  {
-    float ks[NG][2], kz[NG][2], acc[NT][NG][4];
+  const int ka = (r >> 1) + 4 * (r & 1);
+  float sc[NT][KH][2];  // [key ka + 8 h][row i]
+  uint32_t vsz[NG][KH];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t* pk = reinterpret_cast<const uint32_t*>(st + C::OFF_KS) + (ka + 8 * h) * NG;
-      const uint32_t* pv = reinterpret_cast<const uint32_t*>(st + C::OFF_VS) + (ka + 8 * h) * NG;
-      const bool on = !MASKED || (held && ka + 8 * h < left);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t k = on ? pk[g] : 0u, v = on ? pv[g] : 0u;
-        ks[g][h] = lo_f(k), kz[g][h] = hi_f(k);
-        vs[g][h] = lo_f(v), vz[g][h] = hi_f(v);
-      }
-    }
+  for (int s = 0; s < C::HALVES; ++s) {
+    float acc[NT][NG][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const uint2 x = *reinterpret_cast<const uint2*>(st + ka * (D / 2) + g * 32 + c * 8);
-      const uint2 y = *reinterpret_cast<const uint2*>(st + (ka + 8) * (D / 2) + g * 32 + c * 8);
+      const uint2 x = *reinterpret_cast<const uint2*>(st + (ka + 16 * s) * (D / 2) + g * 32 + c * 8);
+      const uint2 y = *reinterpret_cast<const uint2*>(st + (ka + 16 * s + 8) * (D / 2) + g * 32 + c * 8);
       const uint32_t wx[4] = {x.x, x.x >> 8, x.y, x.y >> 8}, wy[4] = {y.x, y.x >> 8, y.y, y.y >> 8};
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j][g][0] = acc[j][g][1] = acc[j][g][2] = acc[j][g][3] = 0.f;
@@ -271,123 +272,223 @@ __device__ __forceinline__ void q4_slice(const uint8_t* st, int k0, int lane, bo
       }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int e = 0; e < 2; ++e) {
+      const int h = 2 * s + e;
+      const uint32_t* pk = reinterpret_cast<const uint32_t*>(st + C::OFF_KS) + (ka + 8 * h) * NG;
+      const uint32_t* pv = reinterpret_cast<const uint32_t*>(st + C::OFF_VS) + (ka + 8 * h) * NG;
+      const bool on = !MASKED || ka + 8 * h < left;
+      uint32_t ksz[NG];
+      if constexpr (NG == 2) {
+        const uint2 k = *reinterpret_cast<const uint2*>(pk), v = *reinterpret_cast<const uint2*>(pv);
+        ksz[0] = k.x, ksz[1] = k.y, vsz[0][h] = v.x, vsz[1][h] = v.y;
+      } else {
+        ksz[0] = *pk, vsz[0][h] = *pv;
+      }
+      if (!on) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int g = 0; g < NG; ++g) ksz[g] = vsz[g][h] = 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = acc[j][0][2 * h + i] * ks[0][h], y = kz[0][h] * R.sum[j][0][i];
+          float x = acc[j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
 #pragma unroll
           for (int g = 1; g < NG; ++g) {
-            x = fmaf(acc[j][g][2 * h + i], ks[g][h], x);
-            y = fmaf(kz[g][h], R.sum[j][g][i], y);
+            x = fmaf(acc[j][g][2 * e + i], lo_f(ksz[g]), x);
+            y = fmaf(hi_f(ksz[g]), R.sum[j][g][i], y);
           }
           sc[j][h][i] = fmaf(x, R.qs[j][i], y);
         }
       }
     }
   }
-  bool seen[NT][2][2], higher = false;
+  bool seen[NT][KH][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int h = 0; h < KH; ++h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int i = 0; i < 2; ++i) {
         seen[j][h][i] =
             !MASKED || (ka + 8 * h < left && ka + 8 * h < open + (row0 + j * 8 + 2 * c + i) / G - row0 / G);
         if (!seen[j][h][i]) sc[j][h][i] = -INFINITY;
       }
-      // The maximum follows once a logit is 2^3 times above it: p up to 8 costs
-      // fp32 nothing, and most slices pass.
-      higher = higher || fmaxf(sc[j][0][i], sc[j][1][i]) > S.m[j][i] + 3.f;
     }
   }
-  if (__any_sync(0xffffffffu, higher)) {
+  // p and, in f16, p s times its power of two. The maximum follows a logit that
+  // is more than 2^3 times above it (p up to 8 costs fp32 nothing), the power a p s of
+  // 2^15 or more: most steps change neither.
+  float p[NT][KH][2];
+  uint32_t ph[NT][NG][KH];
+  auto weigh = [&]() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int h = 0; h < KH; ++h) {
+        const float p0 = ex2(sc[j][h][0] - S.m[j][0]), p1 = ex2(sc[j][h][1] - S.m[j][1]);
+        p[j][h][0] = p0, p[j][h][1] = p1;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)  // (a hidden key's scale may be NaN)
+          ph[j][g][h] = pack_f16x2((seen[j][h][0] ? p0 * lo_f(vsz[g][h]) : 0.f) * S.up[j][g][0],
+                                   (seen[j][h][1] ? p1 * lo_f(vsz[g][h]) : 0.f) * S.up[j][g][1]);
+      }
+    }
+  };
+  weigh();
+  float most = 0.f;
+  uint32_t most_h = 0u;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int h = 0; h < KH; ++h) {
+      most = max3f(most, p[j][h][0], p[j][h][1]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) most_h = max_f16x2(most_h, ph[j][g][h]);
+    }
+  }
+  if (__any_sync(0xffffffffu, most > 8.f || ((most_h + 0x08000800u) & 0x80008000u) != 0u)) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float mn = column_max(fmaxf(fmaxf(sc[j][0][i], sc[j][1][i]), S.m[j][i]));
+        float mn = S.m[j][i];
+#pragma unroll
+        for (int h = 0; h < KH; ++h) mn = fmaxf(mn, sc[j][h][i]);
+        mn = column_max(mn);
         const float alpha = ex2(S.m[j][i] - mn);
         S.m[j][i] = mn;
         S.l[j][i] *= alpha;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           S.z[j][g][i] *= alpha;
+          float f = alpha, mx = 0.f;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) S.o[j][g][t][i] *= alpha, S.o[j][g][t][2 + i] *= alpha;
+          for (int h = 0; h < KH; ++h)
+            if (seen[j][h][i]) mx = fmaxf(mx, ex2(sc[j][h][i] - mn) * lo_f(vsz[g][h]));
+          mx = column_max(mx);
+          if (mx * S.up[j][g][i] >= 0x1p15f) {  // (the same in all lanes of the column)
+            const float up = pow2(min(9 - exponent(mx), 120));
+            f *= up / S.up[j][g][i];
+            S.up[j][g][i] = up;
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) S.o[j][g][t][i] *= f, S.o[j][g][t][2 + i] *= f;
         }
       }
     }
+    weigh();
   }
-  float ps[NT][NG][2][2];  // [group][key][row]: p s
-  bool over = false;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float p[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        p[h] = ex2(sc[j][h][i] - S.m[j][i]);
-        S.l[j][i] += p[h];
-      }
+      for (int h = 0; h < KH; ++h) {
+        S.l[j][i] += p[j][h][i];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ps[j][g][h][i] = seen[j][h][i] ? p[h] * vs[g][h] : 0.f;  // a hidden key's scale may be NaN
-          S.z[j][g][i] = fmaf(p[h], seen[j][h][i] ? vz[g][h] : 0.f, S.z[j][g][i]);
-        }
-        over = over || fmaxf(ps[j][g][0][i], ps[j][g][1][i]) * S.up[j][g][i] > 0x1p15f;
-      }
-    }
-  }
-  if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mx = column_max(fmaxf(ps[j][g][0][i], ps[j][g][1][i]));
-          if (mx * S.up[j][g][i] > 0x1p15f) {  // (the same in all lanes of the column)
-            const float up = pow2(min(9 - exponent(mx), 120)), f = up / S.up[j][g][i];
-            S.up[j][g][i] = up;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) S.o[j][g][t][i] *= f, S.o[j][g][t][2 + i] *= f;
-          }
-        }
+        for (int g = 0; g < NG; ++g)
+          S.z[j][g][i] = fmaf(p[j][h][i], seen[j][h][i] ? hi_f(vsz[g][h]) : 0.f, S.z[j][g][i]);
       }
     }
   }
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    uint32_t bp[NT][2];
+  for (int s = 0; s < C::HALVES; ++s) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        bp[j][h] = transpose8(pack_f16x2(ps[j][g][h][0] * S.up[j][g][0], ps[j][g][h][1] * S.up[j][g][1]));
-    }
-    // Word r of the group of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (as k indices).
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = *reinterpret_cast<const uint32_t*>(st + C::OFF_VC + (k0 + c + 4 * (i & 1) + 8 * (i >> 1)) * (D / 2) +
-                                                g * 32 + r * 4);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      // Byte t of both keys of a pair: dimensions 8 r + 2 t (rows 0 .. 7) and 8 r + 2 t + 1 (rows 8 .. 15).
-      const uint32_t x = __byte_perm(w[0], w[1], t | t << 4 | (4 + t) << 8 | (4 + t) << 12);
-      const uint32_t y = __byte_perm(w[2], w[3], t | t << 4 | (4 + t) << 8 | (4 + t) << 12);
+    for (int g = 0; g < NG; ++g) {
+      uint32_t bp[NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        mma_f16(S.o[j][g][t], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, bp[j][0], bp[j][1]);
+        bp[j][0] = transpose8(ph[j][g][2 * s]), bp[j][1] = transpose8(ph[j][g][2 * s + 1]);
+      // Word r of the group of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (as k indices).
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = *reinterpret_cast<const uint32_t*>(
+            st + C::OFF_VC + (16 * s + c + 4 * (i & 1) + 8 * (i >> 1)) * (D / 2) + g * 32 + r * 4);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        // Byte t of both keys of a pair: dimensions 8 r + 2 t (rows 0 .. 7) and 8 r + 2 t + 1 (rows 8 .. 15).
+        const uint32_t x = __byte_perm(w[0], w[1], t | t << 4 | (4 + t) << 8 | (4 + t) << 12);
+        const uint32_t y = __byte_perm(w[2], w[3], t | t << 4 | (4 + t) << 8 | (4 + t) << 12);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          mma_f16(S.o[j][g][t], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, bp[j][0],
+                  bp[j][1]);
+      }
     }
   }
 }
+
+// A warp's copies: its keys of the CTA's tiles, in order, across items. Lane i
+// holds where the 16 keys of the i-th half from tile `base` on lie; in a copy
+// the warp's lower half takes the first 16 keys of the stage, the upper one the
+// other 16.
+template <int D, int NT>
+struct Q4Copies {
+  using C = Q4Cfg<D, NT>;
+  Q4Walk w;
+  int at, base, upto;  // the next tile of the item to copy; the tiles whose places the lanes hold
+  long long row;       // this lane's: (block, key head, slot) of the first key; -1: nowhere
+  bool more;
+  const uint8_t *kc, *vc, *sc;  // the cache, at this lane's 16 bytes
+  uint32_t dst;                 // and the ring
+  __device__ __forceinline__ void begin(const Q4DecodeArgs& a, const Q4Walk& first, uint32_t ring, int warp, int lane) {
+    w = first;
+    more = true;
+    at = w.tile;
+    const int i = lane & 15, half = lane >> 4;
+    kc = a.k_codes + i * 16;
+    vc = a.v_codes + i * 16;
+    constexpr int SL = 16 * C::NG * 4 / 16;  // lanes of 16 keys' scales of K, then of V
+    sc = (i < SL ? a.k_scales : a.v_scales) + i % SL * 16;
+    dst = ring + half * (C::CODE_BYTES / 2) + i * 16;
+    look(a, warp, lane);
+  }
+  __device__ __forceinline__ void look(const Q4DecodeArgs& a, int warp, int lane) {
+    base = at;
+    upto = min(at + 32 / C::HALVES, w.tile + w.here);
+    const int tile = at + lane / C::HALVES;
+    const int key = tile * kQ4Tile + warp * C::KEYS + lane % C::HALVES * 16;
+    row = -1;
+    if (tile < upto && key < w.L) {
+      const int block = key / a.block_size;
+      const int phys = a.block_table[static_cast<long long>(w.b) * a.max_blocks + block];
+      if (phys >= 0 && phys < a.num_blocks)
+        row = (static_cast<long long>(phys) * a.Hk + w.item / a.row_blocks) * a.block_size + (key - block * a.block_size);
+    }
+  }
+  // The next tile's keys into stage s (an empty group past the end).
+  __device__ __forceinline__ void copy(const Q4DecodeArgs& a, int s, int warp, int lane) {
+    if (more && at == upto) {
+      if (at == w.tile + w.here) {
+        more = w.next(a);
+        at = w.tile;
+      }
+      if (more) look(a, warp, lane);
+    }
+    if (more) {
+      const long long from = __shfl_sync(0xffffffffu, row, (at - base) * C::HALVES + (lane >> 4));
+      const bool on = from >= 0;
+      const long long f = on ? from * (D / 2) : 0;
+      const uint32_t d = dst + s * C::STAGE_BYTES;
+      constexpr int N = C::CODE_BYTES / 2 / 256;
+#pragma unroll
+      for (int i = 0; i < N; ++i) cp_async16(d + i * 256, kc + f + i * 256, on);
+#pragma unroll
+      for (int i = 0; i < N; ++i) cp_async16(d + C::OFF_VC + i * 256, vc + f + i * 256, on);
+      constexpr int SL = 16 * C::NG * 4 / 16;
+      const int i = lane & 15, half = lane >> 4;
+      // (The scales take an eighth of the codes' bytes.)
+      if (i < 2 * SL)
+        cp_async16(d - half * (C::CODE_BYTES / 2) - i * 16 + (i < SL ? C::OFF_KS : C::OFF_VS) + half * (SL * 16) +
+                       i % SL * 16,
+                   sc + (f >> 3), on);
+      ++at;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
 
 }  // namespace
 
@@ -396,23 +497,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   using C = Q4Cfg<D, NT>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* empty = full + C::STAGES;
-  uint32_t* held_bits = reinterpret_cast<uint32_t*>(smem + C::OFF_SCAN);  // per stage: slices whose block is in the pool
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(held_bits + C::STAGES);
-  int* warp_sum = reinterpret_cast<int*>(held_bits + C::STAGES + 1);
-  int* found = warp_sum + C::CWARPS + 1;  // sequence of the CTA's first tile, tiles of those before it
+  int* warp_sum = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  int* found = warp_sum + C::WARPS;  // sequence of the CTA's first tile, tiles of those before it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) griddep_launch_dependents();
 
-  if (threadIdx.x == 0) {
-    griddep_launch_dependents();
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::CWARPS);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   // The tiles of all sequences, and the sequence that this CTA's run starts in:
   // each thread adds up a stretch of sequences, then their sums are scanned.
   const int items = a.Hk * a.row_blocks;  // of a sequence
@@ -430,9 +519,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   __syncthreads();
   int total = 0, before = upto - own;
 #pragma unroll
-  for (int w = 0; w <= C::CWARPS; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
+  for (int v = 0; v < C::WARPS; ++v) {
+    if (v < warp) before += warp_sum[v];
+    total += warp_sum[v];
   }
   total *= items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), total);  // one tile each at least
@@ -453,173 +542,126 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     w.tile = rem - w.item * n;
     w.enter(a);
   }
-
-  if (warp == C::CWARPS) {
-    // ----------------------------------------------------------- copy warp
-    if (lane == 0) {
-      // For the kernel that joins: whether this CTA is the second one of a cut item.
-      int4 cut = make_int4(-1, 0, 0, 0);
-      if (w.left > 0 && w.tile > 0) {
-        const int first = start - w.tile, prev = q4_share(cta - 1, total, ctas);
-        if (prev <= first)
-          cut = make_int4(w.b, w.item, prev == first ? 0 : 1,
-                          static_cast<int>((static_cast<long long>(first + w.n) * ctas - 1) / total));
-      }
-      a.cuts[cta] = cut;
+  if (threadIdx.x == 0) {
+    // For the kernel that joins: whether this CTA is the second one of a cut item.
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (w.left > 0 && w.tile > 0) {
+      const int first = start - w.tile, prev = q4_share(cta - 1, total, ctas);
+      if (prev <= first)
+        cut = make_int4(w.b, w.item, prev == first ? 0 : 1,
+                        static_cast<int>((static_cast<long long>(first + w.n) * ctas - 1) / total));
     }
-    if (w.left <= 0 || g_test_drop_loads) return;
-    // Lane (piece, array): one copy of `piece` keys of the codes or scales of K or V.
-    const int p = lane >> 2, arr = lane & 3;
-    const int row_bytes = (arr & 1) ? NG * 4 : D / 2;
-    const uint8_t* base = arr == 0 ? a.k_codes : (arr == 1 ? a.k_scales : (arr == 2 ? a.v_codes : a.v_scales));
-    const int dst0 = (arr == 0 ? 0 : (arr == 1 ? C::OFF_KS : (arr == 2 ? C::OFF_VC : C::OFF_VS))) +
-                     p * a.piece * row_bytes;
-    int issued = 0;
-    bool ok = true;
-    do {
-      const int kvh = w.item / a.row_blocks;
-      for (int t = 0; t < w.here && ok; ++t, ++issued) {
-        const int s = issued % C::STAGES;
-        const int key = (w.tile + t) * C::TK + p * a.piece;
-        const bool mine = p * a.piece < C::TK && key < w.L;
-        int phys = -1, block = 0;
-        if (mine) {
-          block = key / a.block_size;
-          phys = a.block_table[static_cast<long long>(w.b) * a.max_blocks + block];
-        }
-        const bool held = mine && phys >= 0 && phys < a.num_blocks;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, held && arr == 0);
-        if (issued >= C::STAGES &&
-            !__all_sync(0xffffffffu, mbar_wait(&empty[s], (issued / C::STAGES - 1) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          uint32_t bits = 0u;  // of 16-key slices
-          for (int i = 0; i < C::TK / 16; ++i) bits |= ((lanes >> (i * 16 / a.piece * 4)) & 1u) << i;
-          held_bits[s] = bits;
-          mbar_arrive_expect_tx(&full[s], __popc(lanes) * a.piece * 2 * (D / 2 + NG * 4));
-        }
-        __syncwarp();
-        if (held) {
-          const long long row = (static_cast<long long>(phys) * a.Hk + kvh) * a.block_size + (key - block * a.block_size);
-          bulk_load(smem + s * C::STAGE_BYTES + dst0, base + row * row_bytes, a.piece * row_bytes, &full[s]);
-        }
-      }
-    } while (ok && w.next(a));
-    // Do not leave with copies in flight (matters only after an abort, when
-    // the consumers stopped waiting; every issued copy lands).
-    if (lane == 0)
-      for (int t = max(0, issued - C::STAGES); t < issued; ++t)
-        mbar_wait_drain(&full[t % C::STAGES], (t / C::STAGES) & 1);
-    return;
+    a.cuts[cta] = cut;
   }
 
-  // -------------------------------------------------------- consumer warps
-  const int r = lane >> 2, c = lane & 3;
-  const int G = a.H / a.Hk;
-  float* red_o = reinterpret_cast<float*>(smem + C::OFF_RED);  // [warp][ROWS][RED_STRIDE]
-  float* red_ml = reinterpret_cast<float*>(smem + C::OFF_ML);  // [warp][ROWS][2]
-  int taken = 0;
-  bool ok = true, first_item = true;
-  if (w.left > 0) do {
-    const int kvh = w.item / a.row_blocks, row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
-    const int rows = min(a.n_new * G - row0, C::ROWS);
-    Q4Rows<D, NT> R;
-    q4_load_rows<D, NT>(a, w.b, kvh, row0, rows, lane, R);
-    Q4State<D, NT> S;
-    S.clear();
-    const int open = w.L - a.n_new + 1 + row0 / G;  // keys from here on are hidden from some row
-    for (int t = 0; t < w.here; ++t, ++taken) {
-      const int s = taken % C::STAGES;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (taken / C::STAGES) & 1, abort_flag));
-      if (!ok) break;
-      const uint8_t* st = smem + s * C::STAGE_BYTES;
-      const int first = (w.tile + t) * C::TK, left = w.L - first;
-      const uint32_t held = held_bits[s];
-#pragma unroll 1
-      for (int k0 = warp * 16; k0 < min(C::TK, left); k0 += C::CWARPS * 16) {
-        const bool on = (held >> (k0 / 16)) & 1u;
-        if (on && k0 + 16 <= min(open - first, left)) q4_slice<D, NT, false>(st, k0, lane, true, left, 0, 0, 1, R, S);
-        else q4_slice<D, NT, true>(st, k0, lane, on, left, open - first, row0, G, R, S);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
-    }
+  if (w.left > 0) {
+    const uint8_t* ring = smem + warp * (C::STAGES * C::STAGE_BYTES);
+    Q4Copies<D, NT> copies;
+    copies.begin(a, w, smem_u32(ring), warp, lane);
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
+    for (int s = 0; s < C::STAGES - 1; ++s) copies.copy(a, s, warp, lane);
+    const int r = lane >> 2, c = lane & 3;
+    const int G = a.H / a.Hk;
+    float* red_o = reinterpret_cast<float*>(smem + C::OFF_RED);  // [warp][ROWS][RED_STRIDE]
+    float* red_ml = reinterpret_cast<float*>(smem + C::OFF_ML);  // [warp][ROWS][2]
+    int stage = 0;
+    bool first_item = true;
+    do {
+      const int kvh = w.item / a.row_blocks, row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
+      const int rows = min(a.n_new * G - row0, C::ROWS);
+      Q4Rows<D, NT> R;
+      q4_load_rows<D, NT>(a, w.b, kvh, row0, rows, lane, R);
+      Q4State<D, NT> S;
+      S.clear();
+      // Of the tile's keys of this warp: those in the sequence, and those that every row sees.
+      int left = w.L - w.tile * kQ4Tile - warp * C::KEYS;
+      int open = left - a.n_new + 1 + row0 / G;
+      for (int t = 0; t < w.here; ++t) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+        __syncwarp();  // every lane's copies have landed, and the stage that is filled next has been read
+        copies.copy(a, stage == 0 ? C::STAGES - 1 : stage - 1, warp, lane);
+        const uint8_t* st = ring + stage * C::STAGE_BYTES;
+        stage = stage == C::STAGES - 1 ? 0 : stage + 1;
+        if (open >= C::KEYS) q4_step<D, NT, false>(st, lane, 0, 0, 0, 1, R, S);
+        else if (left > 0) q4_step<D, NT, true>(st, lane, left, open, row0, G, R, S);
+        left -= kQ4Tile, open -= kQ4Tile;
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            S.l[j][i] += __shfl_xor_sync(0xffffffffu, S.l[j][i], off);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) S.z[j][g][i] += __shfl_xor_sync(0xffffffffu, S.z[j][g][i], off);
+          }
+        }
+      }
+      // Join the warps, once all of them have read what they joined last.
+      __syncthreads();
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          S.l[j][i] += __shfl_xor_sync(0xffffffffu, S.l[j][i], off);
+          const int row = warp * C::ROWS + j * 8 + 2 * c + i;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) S.z[j][g][i] += __shfl_xor_sync(0xffffffffu, S.z[j][g][i], off);
+          for (int g = 0; g < NG; ++g) {
+            const float f = 1.f / S.up[j][g][i];
+            const float f0 = f * 0x1p24f, f1 = f * 0x1p20f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              *reinterpret_cast<float2*>(&red_o[row * C::RED_STRIDE + g * 64 + r * 8 + t * 2]) =
+                  make_float2(fmaf(S.o[j][g][t][i], f0, S.z[j][g][i]), fmaf(S.o[j][g][t][2 + i], f1, S.z[j][g][i]));
+          }
+          if (r == 0) *reinterpret_cast<float2*>(&red_ml[row * 2]) = make_float2(S.m[j][i], S.l[j][i]);
         }
       }
-    }
-    // Join the warps, once all of them have read what they joined last.
-    named_bar_sync(1, C::CWARPS * 32);
+      __syncthreads();
+      const bool whole = w.here == w.n;
+      const int slot = 2 * cta + (first_item ? 0 : 1);
+      for (int x = threadIdx.x / (D / 4); x < rows; x += C::THREADS / (D / 4)) {
+        const int col = threadIdx.x % (D / 4) * 4;
+        float M = kNoLogit;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+        for (int v = 0; v < C::WARPS; ++v) M = fmaxf(M, red_ml[(v * C::ROWS + x) * 2]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = warp * C::ROWS + j * 8 + 2 * c + i;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const float f = 1.f / S.up[j][g][i];
-          const float f0 = f * 0x1p24f, f1 = f * 0x1p20f;
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            *reinterpret_cast<float2*>(&red_o[row * C::RED_STRIDE + g * 64 + r * 8 + t * 2]) =
-                make_float2(fmaf(S.o[j][g][t][i], f0, S.z[j][g][i]), fmaf(S.o[j][g][t][2 + i], f1, S.z[j][g][i]));
+        for (int v = 0; v < C::WARPS; ++v) {
+          const float2 ml = *reinterpret_cast<const float2*>(&red_ml[(v * C::ROWS + x) * 2]);
+          const float f = ex2(ml.x - M);
+          const float4 y = *reinterpret_cast<const float4*>(&red_o[(v * C::ROWS + x) * C::RED_STRIDE + col]);
+          sum = fmaf(ml.y, f, sum);
+          acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
+          acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
         }
-        if (r == 0) *reinterpret_cast<float2*>(&red_ml[row * 2]) = make_float2(S.m[j][i], S.l[j][i]);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+        if (whole) {
+          const long long row = q4_row(a, w.b, kvh, row0 + x);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + col) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (col == 0) a.lse[row] = lse2 * kLn2;
+        } else {
+          const size_t at = static_cast<size_t>(slot) * C::ROWS + x;
+          *reinterpret_cast<float4*>(a.part_o + at * D + col) =
+              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (col == 0) a.part_lse[at] = lse2;
+        }
       }
-    }
-    named_bar_sync(1, C::CWARPS * 32);
-    const bool whole = w.here == w.n;
-    const int slot = 2 * cta + (first_item ? 0 : 1);
-    for (int x = threadIdx.x / (D / 4); x < rows; x += C::CWARPS * 32 / (D / 4)) {
-      const int col = threadIdx.x % (D / 4) * 4;
-      float M = kNoLogit;
-#pragma unroll
-      for (int v = 0; v < C::CWARPS; ++v) M = fmaxf(M, red_ml[(v * C::ROWS + x) * 2]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int v = 0; v < C::CWARPS; ++v) {
-        const float2 ml = *reinterpret_cast<const float2*>(&red_ml[(v * C::ROWS + x) * 2]);
-        const float f = ex2(ml.x - M);
-        const float4 y = *reinterpret_cast<const float4*>(&red_o[(v * C::ROWS + x) * C::RED_STRIDE + col]);
-        sum = fmaf(ml.y, f, sum);
-        acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
-        acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const float lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
-      if (whole) {
-        const long long row = q4_row(a, w.b, kvh, row0 + x);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + col) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (col == 0) a.lse[row] = lse2 * kLn2;
-      } else {
-        const size_t at = static_cast<size_t>(slot) * C::ROWS + x;
-        *reinterpret_cast<float4*>(a.part_o + at * D + col) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (col == 0) a.part_lse[at] = lse2;
-      }
-    }
-    first_item = false;
-  } while (ok && w.next(a));
+      first_item = false;
+    } while (w.next(a));
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
   // Sequences without keys have no tiles: every CTA writes its share of their rows.
   for (int b = cta; b < a.B; b += gridDim.x) {
     if (q4_len(a, b) > 0) continue;
     const long long row = static_cast<long long>(b) * a.n_new * a.H;
     const int n = a.n_new * a.H;
-    for (int x = threadIdx.x; x < n * (D / 8); x += C::CWARPS * 32)
+    for (int x = threadIdx.x; x < n * (D / 8); x += C::THREADS)
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + row * D)[x] = make_uint4(0u, 0u, 0u, 0u);
-    for (int x = threadIdx.x; x < n; x += C::CWARPS * 32) a.lse[row + x] = -INFINITY;
+    for (int x = threadIdx.x; x < n; x += C::THREADS) a.lse[row + x] = -INFINITY;
   }
 }
 
@@ -681,7 +723,6 @@ __global__ void __launch_bounds__(128) fa_decode_q4_join_kernel(const Q4DecodeAr
 template <int D, int NT>
 static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks) {
   using C = Q4Cfg<D, NT>;
-  static_assert(C::CTAS * 152 <= kQ4MaxCtas, "the workspace holds the parts of every CTA");
   auto kern = fa_decode_q4_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -701,11 +742,5 @@ cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const L
   if (a.rows_per == 8) return a.D == 64 ? launch_q4_t<64, 1>(a, stream, m) : launch_q4_t<128, 1>(a, stream, m);
   return a.D == 64 ? launch_q4_t<64, 2>(a, stream, m) : launch_q4_t<128, 2>(a, stream, m);
 }
-
-cudaError_t set_decode_q4_test_hooks(unsigned long long wait_limit_ns, int drop_loads, cudaStream_t stream) {
-  return set_test_hooks_here(wait_limit_ns, drop_loads, stream);
-}
-
-int take_decode_q4_status() { return take_status_here(); }
 
 }  // namespace fa

@@ -293,9 +293,7 @@ def test_captured_and_on_two_streams():
 
 
 @pytest.mark.gpu
-def test_waits_run_out_then_context_recovers(monkeypatch):
-    """Dropped loads with a 2 ms bound: the kernel gives up and says so, and
-    the context computes again. Nothing is allocated by a call."""
+def test_a_call_allocates_nothing():
     import torch
     for d in (64, 128):
         for lens, n, H in (([900, 40], 1, 8), ([300], 7, 4)):
@@ -310,14 +308,7 @@ def test_waits_run_out_then_context_recovers(monkeypatch):
                 binding.fa_decode_paged_q4(*a[:5], o, lse, *a[5:], ws)
             torch.cuda.synchronize()
             assert torch.cuda.mem_get_info()[0] == free
-            monkeypatch.setenv("FA_TEST_WAIT_LIMIT_NS", "2000000")
-            monkeypatch.setenv("FA_TEST_DROP_LOADS", "1")
-            binding.fa_decode_paged_q4(*a[:5], o, lse, *a[5:], ws)
-            torch.cuda.synchronize()
-            assert binding.fa_check_status() == binding.FA_ERR_TIMEOUT
-            monkeypatch.delenv("FA_TEST_WAIT_LIMIT_NS")
-            monkeypatch.delenv("FA_TEST_DROP_LOADS")
-            x.check(*x.run())
+            x.check(o, lse)
 
 
 FAKE = 0x10000
