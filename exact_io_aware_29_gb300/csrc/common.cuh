@@ -298,6 +298,7 @@ struct Q4DecodeArgs {
   int4* cuts;                 // [kQ4MaxCtas]: (sequence or -1, item of it, part of the CTA before it, last CTA)
 };
 constexpr int kQ4Tile = 128;           // keys of a tile
+constexpr int kQ4Head = 3;             // an item's cost besides its tiles, in tiles
 constexpr int kQ4MaxCtas = 4 * 152;    // four per SM
 cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks);
 

@@ -58,7 +58,7 @@ struct Q4Cfg {
   static constexpr int OFF_RED = WARPS * STAGES * STAGE_BYTES;
   static constexpr int OFF_ML = OFF_RED + WARPS * ROWS * RED_STRIDE * 4;
   static constexpr int OFF_SCAN = OFF_ML + WARPS * ROWS * 2 * 4;
-  static constexpr int SMEM_BYTES = OFF_SCAN + WARPS * 4 + 8;
+  static constexpr int SMEM_BYTES = OFF_SCAN + WARPS * 8 + 8;
   static_assert((SMEM_BYTES + 1024) * CTAS <= 228 * 1024, "fits in an SM");
 };
 
@@ -80,6 +80,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 // max(a, b), NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -105,14 +106,22 @@ __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   return min(max(a.seq_lens[b], 0), a.max_seq_len);
 }
 __device__ __forceinline__ int q4_tiles(int L) { return (L + kQ4Tile - 1) / kQ4Tile; }
-// First tile of CTA c's share of `total`.
-__device__ __forceinline__ int q4_share(int c, int total, int ctas) {
-  return static_cast<int>(static_cast<long long>(c) * total / ctas);
-}
+// How `total` units of work are shared out over `ctas` CTAs: runs of `per` or
+// per + 1, the longer ones first. A unit is a tile; an item counts as `head`
+// units more, in front of its tiles.
+struct Q4Shares {
+  int per, longer, head;
+  __device__ __forceinline__ Q4Shares(int total, int ctas, int h) : per(total / ctas), longer(total % ctas), head(h) {}
+  __device__ __forceinline__ int start(int c) const { return c * per + min(c, longer); }
+  __device__ __forceinline__ int of(int unit) const {  // the CTA that has it
+    const int x = longer * (per + 1);
+    return unit < x ? unit / (per + 1) : longer + (unit - x) / per;
+  }
+};
 
-// A CTA's way along its run of tiles [x, end): item by item.
+// A CTA's way along its run, item by item.
 struct Q4Walk {
-  int b, item, tile, left;  // sequence, (key head, row block) of it, first tile in it, tiles of the run from here on
+  int b, item, tile, left;  // sequence, (key head, row block) of it, first tile in it, units of the run from there on
   int L, n;                 // length, tiles and
   int here;                 // tiles of the run in this item
   __device__ __forceinline__ void enter(const Q4DecodeArgs& a) {
@@ -120,8 +129,8 @@ struct Q4Walk {
     n = q4_tiles(L);
     here = min(n - tile, left);
   }
-  __device__ __forceinline__ bool next(const Q4DecodeArgs& a) {  // false at the end of the run
-    left -= here;
+  __device__ __forceinline__ bool next(const Q4DecodeArgs& a, int head) {  // false at the end of the run
+    left -= here + head;
     if (left <= 0) return false;
     tile = 0;
     if (++item < a.Hk * a.row_blocks) {
@@ -369,7 +378,7 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
           mx = column_max(mx);
           if (mx * S.up[j][g][i] >= 0x1p15f) {  // (the same in all lanes of the column)
             const float up = pow2(min(9 - exponent(mx), 120));
-            f *= up / S.up[j][g][i];
+            f *= up * inverse_pow2(S.up[j][g][i]);
             S.up[j][g][i] = up;
           }
 #pragma unroll
@@ -428,13 +437,16 @@ template <int D, int NT>
 struct Q4Copies {
   using C = Q4Cfg<D, NT>;
   Q4Walk w;
+  int head;
   int at, base, upto;  // the next tile of the item to copy; the tiles whose places the lanes hold
   long long row;       // this lane's: (block, key head, slot) of the first key; -1: nowhere
   bool more;
   const uint8_t *kc, *vc, *sc;  // the cache, at this lane's 16 bytes
   uint32_t dst;                 // and the ring
-  __device__ __forceinline__ void begin(const Q4DecodeArgs& a, const Q4Walk& first, uint32_t ring, int warp, int lane) {
+  __device__ __forceinline__ void begin(const Q4DecodeArgs& a, const Q4Walk& first, int h, uint32_t ring, int warp,
+                                        int lane) {
     w = first;
+    head = h;
     more = true;
     at = w.tile;
     const int i = lane & 15, half = lane >> 4;
@@ -462,7 +474,7 @@ struct Q4Copies {
   __device__ __forceinline__ void copy(const Q4DecodeArgs& a, int s, int warp, int lane) {
     if (more && at == upto) {
       if (at == w.tile + w.here) {
-        more = w.next(a);
+        more = w.next(a, head);
         at = w.tile;
       }
       if (more) look(a, warp, lane);
@@ -497,67 +509,78 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   using C = Q4Cfg<D, NT>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
-  int* warp_sum = reinterpret_cast<int*>(smem + C::OFF_SCAN);
-  int* found = warp_sum + C::WARPS;  // sequence of the CTA's first tile, tiles of those before it
+  long long* warp_sum = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
+  int* found = reinterpret_cast<int*>(warp_sum + C::WARPS);  // sequence of the CTA's first tile, units of those before it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  // The tiles of all sequences, and the sequence that this CTA's run starts in:
-  // each thread adds up a stretch of sequences, then their sums are scanned.
+  // The tiles of all sequences (and, in the upper half, how many have any), and
+  // the sequence that this CTA's run starts in: each thread adds up a stretch of
+  // sequences, then their sums are scanned.
   const int items = a.Hk * a.row_blocks;  // of a sequence
   const int stretch = (a.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * stretch, a.B), b1 = min(b0 + stretch, a.B);
-  int own = 0;
-  for (int b = b0; b < b1; ++b) own += q4_tiles(q4_len(a, b));
-  int upto = own;
+  long long own = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = q4_tiles(q4_len(a, b));
+    own += n > 0 ? n + (1LL << 32) : 0;
+  }
+  long long upto = own;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, off);
+    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
     if (lane >= off) upto += x;
   }
   if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  int total = 0, before = upto - own;
+  long long all = 0, before = upto - own;
 #pragma unroll
   for (int v = 0; v < C::WARPS; ++v) {
     if (v < warp) before += warp_sum[v];
-    total += warp_sum[v];
+    all += warp_sum[v];
   }
-  total *= items;
-  const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), total);  // one tile each at least
-  const int start = cta < ctas ? q4_share(cta, total, ctas) : 0, end = cta < ctas ? q4_share(cta + 1, total, ctas) : 0;
-  if (start < end && start / items >= before && start / items < before + own) {
-    int b = b0, x = before;
-    for (int n; x + (n = q4_tiles(q4_len(a, b))) <= start / items; ++b) x += n;
+  // An item costs about two tiles' time besides its tiles (its queries, and the
+  // join of the warps). Where runs are short, what counts is the longest of
+  // them: only tiles then. (64 sequences of up to 8192 tokens: MEASURED)
+  const int tiles = static_cast<int>(all) * items;
+  const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
+  const int head = tiles >= 8 * ctas ? kQ4Head : 0;
+  const Q4Shares shares(tiles + head * static_cast<int>(all >> 32) * items, max(ctas, 1), head);
+  auto units = [&](long long sum) { return (static_cast<int>(sum) + head * static_cast<int>(sum >> 32)) * items; };
+  const int start = shares.start(cta);
+  if (cta < ctas && start >= units(before) && start < units(before + own)) {
+    int b = b0, x = units(before);
+    for (;; ++b) {
+      const int n = q4_tiles(q4_len(a, b)), u = n > 0 ? (n + head) * items : 0;
+      if (x + u > start) break;
+      x += u;
+    }
     found[0] = b, found[1] = x;
   }
   __syncthreads();
   Q4Walk w;
-  w.left = end - start;
-  if (w.left > 0) {
+  w.left = 0;
+  int4 cut = make_int4(-1, 0, 0, 0);
+  if (cta < ctas) {
     w.b = found[0];
-    const int rem = start - found[1] * items;
-    const int n = q4_tiles(q4_len(a, w.b));
-    w.item = rem / n;
-    w.tile = rem - w.item * n;
+    const int rem = start - found[1], u = q4_tiles(q4_len(a, w.b)) + head;
+    w.item = rem / u;
+    const int into = rem - w.item * u;  // units of the item in front of the run
+    w.tile = max(into - head, 0);
+    w.left = shares.start(cta + 1) - start - max(head - into, 0);
     w.enter(a);
-  }
-  if (threadIdx.x == 0) {
-    // For the kernel that joins: whether this CTA is the second one of a cut item.
-    int4 cut = make_int4(-1, 0, 0, 0);
-    if (w.left > 0 && w.tile > 0) {
-      const int first = start - w.tile, prev = q4_share(cta - 1, total, ctas);
-      if (prev <= first)
-        cut = make_int4(w.b, w.item, prev == first ? 0 : 1,
-                        static_cast<int>((static_cast<long long>(first + w.n) * ctas - 1) / total));
+    if (w.tile > 0) {
+      // For the kernel that joins: whether this CTA is the second one of a cut item.
+      const int first = start - into, prev = shares.of(start - 1), at = shares.start(prev);
+      if (at <= first + head) cut = make_int4(w.b, w.item, at >= first ? 0 : 1, shares.of(first + u - 1));
     }
-    a.cuts[cta] = cut;
   }
+  if (threadIdx.x == 0) a.cuts[cta] = cut;
 
   if (w.left > 0) {
     const uint8_t* ring = smem + warp * (C::STAGES * C::STAGE_BYTES);
     Q4Copies<D, NT> copies;
-    copies.begin(a, w, smem_u32(ring), warp, lane);
+    copies.begin(a, w, head, smem_u32(ring), warp, lane);
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) copies.copy(a, s, warp, lane);
     const int r = lane >> 2, c = lane & 3;
@@ -607,7 +630,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
           const int row = warp * C::ROWS + j * 8 + 2 * c + i;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const float f = 1.f / S.up[j][g][i];
+            const float f = inverse_pow2(S.up[j][g][i]);
             const float f0 = f * 0x1p24f, f1 = f * 0x1p20f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
         }
       }
       first_item = false;
-    } while (w.next(a));
+    } while (w.next(a, head));
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   // Sequences without keys have no tiles: every CTA writes its share of their rows.
@@ -665,55 +688,75 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   }
 }
 
-// Joins the parts of cut items: CTA (x, y) takes row y of the item whose second
-// part is grid CTA x's first one. O = sum of 2^(lse_i - M) O_i over the sum of
-// the weights, in the order of the keys: the warps every fourth part, then
-// their sums.
+// Joins the parts of cut items: CTA (x, y) four rows (from 4 y on) of the item
+// whose second part is grid CTA x's first one. O = sum of 2^(lse_i - M) O_i over
+// the sum of the weights, in a fixed order: a row's four warps take every fourth
+// part, then the first adds up theirs. The first four parts of a warp are read
+// along with the sums: with up to 16 parts there are two reads to wait for.
 template <int D>
-__global__ void __launch_bounds__(128) fa_decode_q4_join_kernel(const Q4DecodeArgs a) {
-  constexpr int CPL = D / 32;  // columns per lane
-  __shared__ float red[4][D + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(512) fa_decode_q4_join_kernel(const Q4DecodeArgs a) {
+  constexpr int CPL = D / 32, SUBS = 4, AHEAD = 4;  // columns per lane
+  __shared__ float red[16][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % SUBS, x = blockIdx.y * 4 + warp / SUBS;
   griddep_wait();
   const int4 cut = a.cuts[blockIdx.x];
   if (cut.x < 0) return;
-  const int kvh = cut.y / a.row_blocks, row = (cut.y - kvh * a.row_blocks) * a.rows_per + blockIdx.y;
-  if (row >= a.n_new * (a.H / a.Hk)) return;
-  const int c0 = blockIdx.x - 1, n = cut.w - c0 + 1;
-  auto part = [&](int i) {
-    return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? cut.z : 0)) * a.rows_per + blockIdx.y;
+  const int kvh = cut.y / a.row_blocks, row0 = (cut.y - kvh * a.row_blocks) * a.rows_per;
+  const bool on = x < min(a.n_new * (a.H / a.Hk) - row0, a.rows_per);
+  const int c0 = blockIdx.x - 1, n = on ? cut.w - c0 + 1 : 0;
+  auto part = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? cut.z : 0)) * a.rows_per + x; };
+  struct Part {
+    float lse, y[CPL];
   };
-  float M = -INFINITY;
+  auto read = [&](int i) {
+    Part p;
+    p.lse = a.part_lse[part(i)];
+    const float* src = a.part_o + part(i) * D + lane * CPL;
+    if constexpr (CPL == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      p.y[0] = v.x, p.y[1] = v.y, p.y[2] = v.z, p.y[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      p.y[0] = v.x, p.y[1] = v.y;
+    }
+    return p;
+  };
+  Part first[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (sub + k * SUBS < n) first[k] = read(sub + k * SUBS);
+  float M = -INFINITY, sum = 0.f, acc[CPL];
   for (int i = lane; i < n; i += 32) M = max_nan(M, a.part_lse[part(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float sum = 0.f, acc[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
-  if (M != -INFINITY) {
-#pragma unroll 4
-    for (int i = warp; i < n; i += 4) {
-      const float f = ex2(a.part_lse[part(i)] - M);
-      const float* src = a.part_o + part(i) * D + lane * CPL;
-      sum += f;
+  auto add = [&](const Part& p) {
+    const float f = ex2(p.lse - M);
+    sum += f;
 #pragma unroll
-      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(f, src[k], acc[k]);
-    }
+    for (int k = 0; k < CPL; ++k) acc[k] = fmaf(f, p.y[k], acc[k]);
+  };
+  if (M != -INFINITY) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (sub + k * SUBS < n) add(first[k]);
+#pragma unroll 4
+    for (int i = sub + AHEAD * SUBS; i < n; i += SUBS) add(read(i));
   }
 #pragma unroll
   for (int k = 0; k < CPL; ++k) red[warp][lane * CPL + k] = acc[k];
   if (lane == 0) red[warp][D] = sum;
   __syncthreads();
-  if (warp > 0) return;
-  sum = red[0][D];
+  if (!on || sub > 0) return;
 #pragma unroll
-  for (int v = 1; v < 4; ++v) {
-    sum += red[v][D];
+  for (int v = 1; v < SUBS; ++v) {
+    sum += red[warp + v][D];
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] += red[v][lane * CPL + k];
+    for (int k = 0; k < CPL; ++k) acc[k] += red[warp + v][lane * CPL + k];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const long long at = q4_row(a, cut.x, kvh, row);
+  const long long at = q4_row(a, cut.x, kvh, row0 + x);
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at * D + lane * CPL);
 #pragma unroll
   for (int k = 0; k < CPL; k += 2) out[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
@@ -733,7 +776,8 @@ static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const
   mark(marks, false, 0, stream);
   if (e != cudaSuccess) return e;
   mark(marks, true, 1, stream);
-  e = launch_maybe_pdl(fa_decode_q4_join_kernel<D>, dim3(grid, C::ROWS), dim3(128), 0, stream, marks == nullptr, a);
+  e = launch_maybe_pdl(fa_decode_q4_join_kernel<D>, dim3(grid, (std::min(a.n_new * (a.H / a.Hk), C::ROWS) + 3) / 4),
+                       dim3(512), 0, stream, marks == nullptr, a);
   mark(marks, false, 1, stream);
   return e;
 }
