@@ -31,15 +31,15 @@ __device__ __forceinline__ void words(const uint4& v, uint32_t (&w)[4]) {
   w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
 }
 
-// NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// The larger and the smaller of each pair of bf16, NaN where either is.
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -97,99 +97,92 @@ struct Turn {
 // The eight codes (element i in bits 4 i) of a lane's packed words, and the
 // packed (s, z) of its group, which eight neighbouring lanes hold.
 __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[4], uint32_t& sz) {
-  float lo = min_nan(lo_f(w[0]), hi_f(w[0])), hi = max_nan(lo_f(w[0]), hi_f(w[0]));
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    lo = min_nan(lo, min_nan(lo_f(w[i]), hi_f(w[i])));
-    hi = max_nan(hi, max_nan(lo_f(w[i]), hi_f(w[i])));
-  }
+  uint32_t lo2 = min_nan2(min_nan2(w[0], w[1]), min_nan2(w[2], w[3]));
+  uint32_t hi2 = max_nan2(max_nan2(w[0], w[1]), max_nan2(w[2], w[3]));
+  lo2 = min_nan2(lo2, swap_halves(lo2));
+  hi2 = max_nan2(hi2, swap_halves(hi2));
+  uint32_t ends = (lo2 & 0xFFFFu) | (hi2 & 0xFFFF0000u);  // minimum and maximum
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, ends, off);
+    ends = (min_nan2(ends, x) & 0xFFFFu) | (max_nan2(ends, x) & 0xFFFF0000u);
   }
+  const float lo = lo_f(ends), hi = hi_f(ends);
   // (max - min) / 15 to bf16: the fp32 quotient in between rounds no other way
   // than the exact one would, whose bf16 ties are fp32 numbers times 15.
   uint32_t sb = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 0.f) & 0xFFFFu;
   float s = __uint_as_float(sb << 16);
   if (s < 0x1p-126f) s = 0.f, sb = 0u;  // 1 / s stays finite
-  if (!(s <= 0x1.fep127f)) {            // a NaN, an infinity or a range past fp32: all of the group reads as NaN
-    sz = 0x7FFF7FFFu;
-    return 0u;
-  }
-  sz = sb | (__float_as_uint(lo) & 0xFFFF0000u);
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  const bool bad = !(s <= 0x1.fep127f);  // a NaN, an infinity or a range past fp32: all of the group reads as NaN
+  sz = bad ? 0x7FFF7FFFu : (sb | ends << 16);
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f, half = 0.5f * s;
   uint32_t codes = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = (i & 1) ? hi_f(w[i / 2]) : lo_f(w[i / 2]);
     const float t = __fsub_rn(x, lo);
-    float k = rintf(t * inv);
-    const float r = fmaf(-k, s, t), r2 = r + r;
-    const bool odd = (static_cast<int>(k) & 1) != 0;
-    if (r2 > s || (odd && r2 == s)) k += 1.f;
-    if (r2 < -s || (odd && r2 == -s)) k -= 1.f;
-    codes |= static_cast<uint32_t>(min(max(static_cast<int>(k), 0), 15)) << (4 * i);
+    // k = rint(t / s) but for the quotient's rounding: the integer in the low
+    // bits of a sum with 1.5 2^23. The remainder says whether it is off (a tie
+    // counts where k is odd). t / s <= 15 (1 + 2^-8), so k stays in 0..15.
+    const float kf = fmaf(t, inv, 12582912.f);
+    const int k = __float_as_int(kf);
+    const float r = fmaf(-(kf - 12582912.f), s, t);
+    const int one = (__float_as_int(r) >> 31) | 1;  // -1 or 1, where the remainder points
+    const bool off = fabsf(r) > __int_as_float(__float_as_int(half) - (k & 1));
+    codes |= static_cast<uint32_t>((k + (off ? one : 0)) & 15) << (4 * i);
   }
-  return s > 0.f ? codes : 0u;
-}
-
-// Section and rows of a unit of the append: `n` consecutive heads of one token
-// of q (0), k (1) or v (2).
-struct AppendUnit {
-  long long token;
-  int section, head, n;
-};
-__device__ __forceinline__ AppendUnit append_unit(const KvAppendArgs& a, long long u) {
-  const int per = a.q_slices + 2 * a.k_slices;
-  AppendUnit t;
-  t.token = u / per;
-  int x = static_cast<int>(u - t.token * per);
-  t.section = x < a.q_slices ? 0 : (x < a.q_slices + a.k_slices ? 1 : 2);
-  if (t.section > 0) x -= a.q_slices + (t.section - 1) * a.k_slices;
-  t.head = x * a.rows;
-  t.n = min(a.rows, (t.section == 0 ? a.H : a.Hk) - t.head);
-  return t;
+  return s > 0.f && !bad ? codes : 0u;
 }
 
 }  // namespace
 
-// d/8 lanes own a row, 16 bytes each; a group of lanes takes one unit.
-template <int D, bool INTER, bool Q4>
+// d/8 lanes own a row, 16 bytes each; a group of lanes takes up to R
+// consecutive heads of one token, all read before the first is written. The CTAs
+// of q come first, then those of k and of v.
+template <int D, bool INTER, bool Q4, int R>
 __global__ void __launch_bounds__(256) fa_kv_append_kernel(const KvAppendArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR;
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
-  const long long n_units = a.T * (a.q_slices + 2 * a.k_slices);
-  const long long u = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / LPR;
-  const AppendUnit t = append_unit(a, u < n_units ? u : 0);
-  const int slot = t.section == 0 ? 0 : a.slots[t.token];
+  const int section = static_cast<int>(blockIdx.x) < a.q_ctas ? 0 : (static_cast<int>(blockIdx.x) < a.q_ctas + a.k_ctas ? 1 : 2);
+  const int cta = blockIdx.x - (section == 0 ? 0 : a.q_ctas + (section - 1) * a.k_ctas);
+  const int slices = section == 0 ? a.q_slices : a.k_slices, heads = section == 0 ? a.H : a.Hk;
+  const long long u = static_cast<long long>(cta) * GROUPS + threadIdx.x / LPR;
+  const long long token = min(u / slices, a.T - 1);
+  const int head0 = static_cast<int>(u % slices) * R;
+  const int slot = section == 0 ? 0 : a.slots[token];
   // Slots outside the pool (negative ones mark padding) are not written.
-  const bool live = u < n_units && (t.section == 0 || (slot >= 0 && slot < a.num_blocks * a.block_size));
+  const bool live = u < a.T * slices && (section == 0 || (slot >= 0 && slot < a.num_blocks * a.block_size));
+  const int n = live ? min(R, heads - head0) : 0;
+  const uint16_t* src = static_cast<const uint16_t*>(section == 0 ? a.q : (section == 1 ? a.k : a.v)) +
+                        token * (section == 0 ? a.q_stride : (section == 1 ? a.k_stride : a.v_stride)) +
+                        static_cast<long long>(head0) * D + l * 8;
+  uint4 x[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    x[i] = i < n ? *reinterpret_cast<const uint4*>(src + i * D) : make_uint4(0u, 0u, 0u, 0u);
   Turn<INTER> turn;
-  turn.load(a, t.token, l * 8, lane, live && t.section < 2);
-  const uint16_t* src = static_cast<const uint16_t*>(t.section == 0 ? a.q : (t.section == 1 ? a.k : a.v)) +
-                        t.token * (t.section == 0 ? a.q_stride : (t.section == 1 ? a.k_stride : a.v_stride)) +
-                        static_cast<long long>(t.head) * D + l * 8;
-  for (int i = 0; i < a.rows; ++i) {
-    const bool on = live && i < t.n;
+  if (section < 2) turn.load(a, token, l * 8, lane, live);
+  const int block = slot / a.block_size;
+  // First head's row of the output, in rows of d elements.
+  const long long row = section == 0 ? token * a.H + head0
+                        : Q4 ? (static_cast<long long>(block) * a.Hk + head0) * a.block_size + (slot - block * a.block_size)
+                             : static_cast<long long>(slot) * a.Hk + head0;
+  void* out = section == 0 ? a.q_out : (section == 1 ? a.k_cache : a.v_cache);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
     uint32_t w[4];
-    words(on ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(i) * D) : make_uint4(0u, 0u, 0u, 0u), w);
-    turn.apply(w);
-    const int head = t.head + i;
-    if (!Q4 || t.section == 0) {
-      uint16_t* dst = static_cast<uint16_t*>(t.section == 0 ? a.q_out : (t.section == 1 ? a.k_cache : a.v_cache)) +
-                      ((t.section == 0 ? t.token * a.H : static_cast<long long>(slot) * a.Hk) + head) * D + l * 8;
-      if (on) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if constexpr (Q4) {
+    words(x[i], w);
+    if (section < 2) turn.apply(w);
+    if (!Q4 || section == 0) {
+      if (i < n)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (row + i) * D + l * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
       uint32_t sz;
       const uint32_t codes = quantise(w, sz);
-      if (on && t.section > 0) {
-        const int block = slot / a.block_size;
-        const long long row =
-            (static_cast<long long>(block) * a.Hk + head) * a.block_size + (slot - block * a.block_size);
-        (static_cast<uint32_t*>(t.section == 1 ? a.k_cache : a.v_cache))[row * LPR + l] = codes;
-        if ((l & 7) == 0) (static_cast<uint32_t*>(t.section == 1 ? a.k_scales : a.v_scales))[row * (D / 64) + l / 8] = sz;
+      const long long at = row + static_cast<long long>(i) * a.block_size;
+      if (i < n) {
+        static_cast<uint32_t*>(out)[at * LPR + l] = codes;
+        if ((l & 7) == 0) static_cast<uint32_t*>(section == 1 ? a.k_scales : a.v_scales)[at * (D / 64) + l / 8] = sz;
       }
     }
   }
@@ -238,17 +231,26 @@ __global__ void __launch_bounds__(256) fa_kv_gather_q4_kernel(const KvGatherArgs
   }
 }
 
-template <int D, bool Q4>
-static cudaError_t launch_append_t(KvAppendArgs a, cudaStream_t stream) {
+template <int D, bool Q4, int R>
+static cudaError_t launch_append_r(KvAppendArgs a, cudaStream_t stream) {
   constexpr int kGroups = 256 / (D / 8);
-  a.rows = a.T * (a.H + 2 * a.Hk) >= 152 * 64 ? 4 : 1;
-  a.q_slices = (a.H + a.rows - 1) / a.rows;
-  a.k_slices = (a.Hk + a.rows - 1) / a.rows;
-  const long long grid = (a.T * (a.q_slices + 2 * a.k_slices) + kGroups - 1) / kGroups;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto kern = a.interleaved ? fa_kv_append_kernel<D, true, Q4> : fa_kv_append_kernel<D, false, Q4>;
-  kern<<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+  a.q_slices = std::max((a.H + R - 1) / R, 1);
+  a.k_slices = (a.Hk + R - 1) / R;
+  auto ctas = [&](long long units) { return (units + kGroups - 1) / kGroups; };
+  const long long q = a.H > 0 ? ctas(a.T * a.q_slices) : 0, k = ctas(a.T * a.k_slices);
+  if (q + 2 * k > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  a.q_ctas = static_cast<int>(q);
+  a.k_ctas = static_cast<int>(k);
+  auto kern = a.interleaved ? fa_kv_append_kernel<D, true, Q4, R> : fa_kv_append_kernel<D, false, Q4, R>;
+  kern<<<static_cast<unsigned>(q + 2 * k), 256, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, bool Q4>
+static cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
+  // Four rows to a group of lanes once that leaves two CTAs or more for every SM.
+  return a.T * (a.H + 2 * a.Hk) * (D / 8) >= 152LL * 2 * 256 * 4 ? launch_append_r<D, Q4, 4>(a, stream)
+                                                                 : launch_append_r<D, Q4, 1>(a, stream);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
