@@ -274,7 +274,7 @@ struct KvGatherArgs {
   const int* cu;              // int32 [batch + 1]: packed rows of each sequence
   void *k, *v;                // bf16 [total, Hk, d]
   int batch, Hk, D, total, num_blocks, block_size, max_blocks;
-  int rows, slices;           // set at launch: heads per unit of work, units per row
+  int tokens;                 // set at launch: packed rows of a CTA
 };
 cudaError_t launch_kv_gather_q4(const KvGatherArgs& a, cudaStream_t stream);
 

@@ -188,46 +188,82 @@ __global__ void __launch_bounds__(256) fa_kv_append_kernel(const KvAppendArgs a)
   }
 }
 
-// Rows of the 4-bit cache as bf16, z + s code rounded once: a group of d/8
-// lanes takes up to `rows` heads of one packed row of K or V.
+// The number of entries of cu[0 .. n) that are <= row (cu ascends), by all lanes
+// of a warp: 32 entries a turn.
+__device__ __forceinline__ int count_upto(const int* cu, int n, int row, int lane) {
+  int lo = 0, hi = n;
+  for (;;) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, at < hi && cu[min(at, n - 1)] <= row));
+    if (step <= 1) return lo + c;
+    hi = min(hi, lo + c * step);
+    lo = c > 0 ? lo + (c - 1) * step + 1 : lo;
+    if (lo >= hi) return lo;
+  }
+}
+
+// Rows of the 4-bit cache as bf16, z + s code rounded once (fma.rn.bf16x2: the
+// codes are exact, 128 + code being the bits of a nibble under 128's exponent).
+// A CTA takes `tokens` packed rows: its warps look up where they lie, then
+// groups of d/8 lanes take a token's K or V each, four heads at a time.
+constexpr int kGatherTokens = 32;
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv_gather_q4_kernel(const KvGatherArgs a) {
-  constexpr int LPR = D / 8, GROUPS = 256 / LPR;
-  const int l = threadIdx.x % LPR;
-  const long long u = static_cast<long long>(blockIdx.x) * GROUPS + threadIdx.x / LPR;
-  const long long row = u / (2 * a.slices);
-  if (row >= a.total) return;
-  const int x = static_cast<int>(u - row * (2 * a.slices));
-  const bool is_v = x >= a.slices;
-  const int head = (is_v ? x - a.slices : x) * a.rows;
-  // The sequence of the row: the last b with cu[b] <= row.
-  int lo = 0, hi = a.batch + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu[mid] <= row) lo = mid + 1;
-    else hi = mid;
+  constexpr int LPR = D / 8, GROUPS = 256 / LPR, R = 4;
+  __shared__ long long place[kGatherTokens];  // row of head 0 in the cache; -1: reads as zeros; -2: of no sequence
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = threadIdx.x % LPR;
+  const int row0 = blockIdx.x * a.tokens, count = min(a.tokens, a.total - row0);
+  for (int t = warp; t < count; t += 8) {
+    const int row = row0 + t, b = count_upto(a.cu, a.batch + 1, row, lane) - 1;
+    if (lane > 0) continue;
+    long long at = -2;
+    if (b >= 0 && b < a.batch) {
+      const long long pos = static_cast<long long>(row) - a.cu[b] + (a.starts == nullptr ? 0 : a.starts[b]);
+      at = -1;
+      if (pos >= 0 && pos < static_cast<long long>(a.max_blocks) * a.block_size) {
+        const int page = static_cast<int>(static_cast<unsigned long long>(pos) / static_cast<unsigned>(a.block_size));
+        const int phys = a.block_table[static_cast<long long>(b) * a.max_blocks + page];
+        if (phys >= 0 && phys < a.num_blocks)
+          at = static_cast<long long>(phys) * a.Hk * a.block_size + (pos - static_cast<long long>(page) * a.block_size);
+      }
+    }
+    place[t] = at;
   }
-  const int b = lo - 1;
-  if (b < 0 || b >= a.batch) return;  // a row of no sequence: left as it is
-  const long long pos = row - a.cu[b] + (a.starts == nullptr ? 0 : a.starts[b]);
-  const long long page = pos / a.block_size;
-  int phys = -1;
-  if (pos >= 0 && page < a.max_blocks) phys = a.block_table[static_cast<long long>(b) * a.max_blocks + page];
-  const bool held = phys >= 0 && phys < a.num_blocks;  // others read as zeros
-  const int off = static_cast<int>(pos - page * a.block_size);
-  const uint32_t* codes = static_cast<const uint32_t*>(is_v ? a.v_codes : a.k_codes);
-  const uint32_t* scales = static_cast<const uint32_t*>(is_v ? a.v_scales : a.k_scales);
-  uint16_t* out = static_cast<uint16_t*>(is_v ? a.v : a.k) + row * a.Hk * D + l * 8;
-  for (int h = head; h < min(head + a.rows, a.Hk); ++h) {
-    const long long at = (static_cast<long long>(phys) * a.Hk + h) * a.block_size + off;
-    const uint32_t c = held ? codes[at * LPR + l] : 0u, sz = held ? scales[at * (D / 64) + l / 8] : 0u;
-    const float s = lo_f(sz), z = hi_f(sz);
-    uint32_t w[4];
+  __syncthreads();
+  for (int u = threadIdx.x / LPR; u < 2 * count; u += GROUPS) {
+    const int t = u >> 1;
+    const bool is_v = u & 1;
+    const long long at = place[t];
+    if (at < -1) continue;
+    const uint32_t* codes = static_cast<const uint32_t*>(is_v ? a.v_codes : a.k_codes) + at * LPR + l;
+    const uint32_t* scales = static_cast<const uint32_t*>(is_v ? a.v_scales : a.k_scales) + at * (D / 64) + l / 8;
+    uint16_t* out = static_cast<uint16_t*>(is_v ? a.v : a.k) + static_cast<long long>(row0 + t) * a.Hk * D + l * 8;
+    for (int h0 = 0; h0 < a.Hk; h0 += R) {
+      uint32_t c[R], sz[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = pack_bf16x2(fmaf(static_cast<float>((c >> (8 * i)) & 15u), s, z),
-                         fmaf(static_cast<float>((c >> (8 * i + 4)) & 15u), s, z));
-    *reinterpret_cast<uint4*>(out + static_cast<long long>(h) * D) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < R; ++i) {
+        const bool on = at >= 0 && h0 + i < a.Hk;
+        const long long h = static_cast<long long>(h0 + i) * a.block_size;
+        c[i] = on ? codes[h * LPR] : 0u;
+        sz[i] = on ? scales[h * (D / 64)] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (h0 + i >= a.Hk) break;
+        const uint32_t s2 = __byte_perm(sz[i], 0u, 0x1010), z2 = __byte_perm(sz[i], 0u, 0x3232);
+        uint32_t p[4];  // elements k and k + 4
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t v = ((c[i] >> (4 * k)) & 0x000F000Fu) | 0x43004300u;
+          asm("{\n\t.reg .b32 x;\n\tadd.rn.bf16x2 x, %1, %4;\n\tfma.rn.bf16x2 %0, x, %2, %3;\n\t}"
+              : "=r"(p[k])
+              : "r"(v), "r"(s2), "r"(z2), "r"(0xC300C300u));
+        }
+        *reinterpret_cast<uint4*>(out + static_cast<long long>(h0 + i) * D) =
+            make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                       __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+      }
+    }
   }
 }
 
@@ -260,13 +296,10 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_kv_gather_q4(const KvGatherArgs& args, cudaStream_t stream) {
   KvGatherArgs a = args;
-  a.rows = std::min(a.Hk, 4);
-  a.slices = (a.Hk + a.rows - 1) / a.rows;
-  const int groups = 256 / (a.D / 8);
-  const long long grid = (static_cast<long long>(a.total) * 2 * a.slices + groups - 1) / groups;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (a.D == 64) fa_kv_gather_q4_kernel<64><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
-  else fa_kv_gather_q4_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+  a.tokens = std::min(std::max(a.total / (152 * 4), 1), kGatherTokens);
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.total) + a.tokens - 1) / a.tokens);
+  if (a.D == 64) fa_kv_gather_q4_kernel<64><<<grid, 256, 0, stream>>>(a);
+  else fa_kv_gather_q4_kernel<128><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

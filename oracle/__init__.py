@@ -27,6 +27,7 @@ from .norm_rope import norm_rope_backward, norm_rope_forward  # noqa: F401
 from .shared import shared_prefix_decode_forward  # noqa: F401
 from .kv_cache import (  # noqa: F401
     held_q4,
+    held_q4_bf16,
     q4_decode_forward,
     quantise_q4,
     rotated,

@@ -57,6 +57,20 @@ def held_q4(codes, scales):
     return per[..., 1] + per[..., 0] * codes
 
 
+def held_q4_bf16(codes, scales):
+    """held_q4 rounded once to bf16, however far apart z and s are: a sum that
+    fp64 rounded is first taken to its odd neighbour, which no bf16 tie is."""
+    per = np.repeat(np.asarray(scales, np.float64), GROUP, -2)
+    with np.errstate(invalid="ignore"):
+        z, p = per[..., 1], per[..., 0] * codes
+        x = z + p
+        part = x - z
+        err = (z - (x - part)) + (p - part)
+        even = (np.ascontiguousarray(x).view(np.int64) & 1) == 0
+        towards = np.nextafter(x, np.copysign(np.inf, err))
+        return to_bf16(np.where(even & np.isfinite(err) & (err != 0), towards, x))
+
+
 def unpack_codes(packed):
     """uint8 [..., d / 2] -> integers [..., d]."""
     p = np.asarray(packed).astype(np.int64)

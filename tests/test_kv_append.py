@@ -154,7 +154,7 @@ def check_q4(x):
         assert np.array_equal(got, x.expect(oracle.unpack_codes(as_slots(c0).cpu().numpy()), want))
         got_sz = pu.bf16_tensor_to_f64(as_slots(scales))
         assert np.array_equal(got_sz, x.expect(pu.bf16_tensor_to_f64(as_slots(s0)), sz), equal_nan=True)
-        values.append(oracle.held_q4(got, got_sz).astype(np.float32))
+        values.append(oracle.held_q4_bf16(got, got_sz))
     # Read back as sequences of whole and broken pages, from somewhere inside.
     rng = np.random.default_rng(5)
     B = 4
@@ -174,7 +174,7 @@ def check_q4(x):
             want = np.full((total, x.Hk, x.d), 7.0)
             for b in range(B):
                 at = (0 if first is None else first[b]) + np.arange(lens[b])
-                want[cu[b]:cu[b + 1]] = oracle.to_bf16(val[table[b, at // x.page], at % x.page])
+                want[cu[b]:cu[b + 1]] = val[table[b, at // x.page], at % x.page]
             assert same(got, want)
 
 
