@@ -262,7 +262,7 @@ struct KvAppendArgs {
   void *k_scales, *v_scales;  // 4 bits: bf16 (s, z) [num_blocks, Hk, block_size, d / 64, 2]; nullptr for bf16
   long long T, q_stride, k_stride, v_stride;
   int H, Hk, D, rot, max_pos, num_blocks, block_size, interleaved;  // H = 0: no queries
-  int q_slices, k_slices, q_ctas, k_ctas;  // set at launch: units of work per token, CTAs of q and of k (and of v)
+  int q_slices, k_slices, k_ctas, ratio;  // set at launch: units of work per token, CTAs of k (and of v), of q for each
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
 

@@ -11,10 +11,10 @@
 //
 // 4 bits: 64 consecutive elements share s = bf16((max - min) / 15) and z = min
 // (exact: the elements are bf16) and stand for z + s code, with code the
-// nearest integer to (x - z) / s, ties to even, in 0..15. The quotient is not
-// computed: with k = rint((x - z) * (1 / s)), off by at most one, the remainder
-// (x - z) - k s is exact in one fma (k s has 12 bits) and says which side of
-// the border between two codes x lies on.
+// nearest integer to (x - z) / s, ties to even, in 0..15. No quotient is
+// rounded: a product with a reciprocal that is a little too small gives a
+// candidate that is right or one too low, and a remainder that fp32 holds
+// exactly says which.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -49,12 +49,10 @@ template <bool INTER>
 struct Turn {
   bool on;      // this lane's elements are rotated
   int partner;  // lane of the warp (its own when interleaved)
-  float c[8], s[8];
+  uint64_t c[4], s[4];  // pairs
   __device__ __forceinline__ void load(const KvAppendArgs& a, long long token, int e0, int lane, bool wanted) {
     on = wanted && e0 < a.rot;
     partner = lane;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
     if (!on) return;
     const int half = a.rot / 2;
     const int pos = min(max(a.positions[token], 0), a.max_pos - 1);
@@ -64,7 +62,7 @@ struct Turn {
       const float4 s4 = *reinterpret_cast<const float4*>(a.sin + row + e0 / 2);
       const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = cc[i / 2], s[i] = (i & 1) ? ss[i / 2] : -ss[i / 2];
+      for (int i = 0; i < 4; ++i) c[i] = f2_pack(cc[i], cc[i]), s[i] = f2_pack(-ss[i], ss[i]);
     } else {
       const bool second = e0 >= half;
       const long long at = row + (second ? e0 - half : e0);
@@ -73,9 +71,9 @@ struct Turn {
       for (int h = 0; h < 2; ++h) {
         const float4 c4 = *reinterpret_cast<const float4*>(a.cos + at + 4 * h);
         const float4 s4 = *reinterpret_cast<const float4*>(a.sin + at + 4 * h);
-        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[4 * h + i] = cc[i], s[4 * h + i] = second ? ss[i] : -ss[i];
+        const float sign = second ? 1.f : -1.f;
+        c[2 * h] = f2_pack(c4.x, c4.y), c[2 * h + 1] = f2_pack(c4.z, c4.w);
+        s[2 * h] = f2_pack(sign * s4.x, sign * s4.y), s[2 * h + 1] = f2_pack(sign * s4.z, sign * s4.w);
       }
     }
   }
@@ -87,10 +85,13 @@ struct Turn {
     for (int i = 0; i < 4; ++i) p[i] = INTER ? swap_halves(w[i]) : __shfl_sync(0xffffffffu, w[i], partner);
     if (!on) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = pack_bf16x2(
-          __fadd_rn(__fmul_rn(lo_f(w[i]), c[2 * i]), __fmul_rn(lo_f(p[i]), s[2 * i])),
-          __fadd_rn(__fmul_rn(hi_f(w[i]), c[2 * i + 1]), __fmul_rn(hi_f(p[i]), s[2 * i + 1])));
+    for (int i = 0; i < 4; ++i) {
+      // (Packed products with scalar sums: a packed product and sum are contracted into one rounding.)
+      float x0, x1, y0, y1;
+      f2_unpack(f2_mul(f2_pack(lo_f(w[i]), hi_f(w[i])), c[i]), x0, x1);
+      f2_unpack(f2_mul(f2_pack(lo_f(p[i]), hi_f(p[i])), s[i]), y0, y1);
+      w[i] = pack_bf16x2(__fadd_rn(x0, y0), __fadd_rn(x1, y1));
+    }
   }
 };
 
@@ -108,47 +109,73 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[4], uint32_t& s
     ends = (min_nan2(ends, x) & 0xFFFFu) | (max_nan2(ends, x) & 0xFFFF0000u);
   }
   const float lo = lo_f(ends), hi = hi_f(ends);
-  // (max - min) / 15 to bf16: the fp32 quotient in between rounds no other way
-  // than the exact one would, whose bf16 ties are fp32 numbers times 15.
-  uint32_t sb = pack_bf16x2(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 0.f) & 0xFFFFu;
-  float s = __uint_as_float(sb << 16);
-  if (s < 0x1p-126f) s = 0.f, sb = 0u;  // 1 / s stays finite
-  const bool bad = !(s <= 0x1.fep127f);  // a NaN, an infinity or a range past fp32: all of the group reads as NaN
+  // s: the bf16 number below the product, or the next one if the range is over
+  // 15 times their midpoint (13 bits: exact), or just that and the lower one odd.
+  const float range = __fsub_rn(hi, lo);
+  uint32_t sb = __float_as_uint(range * (1.f / 15.f)) >> 16;
+  const float border = 15.f * __uint_as_float(sb << 16 | 0x8000u);
+  if (range > border || (range == border && (sb & 1u))) ++sb;
+  if (sb < 0x80u) sb = 0u;         // below 2^-126, whose reciprocal is not finite
+  const bool bad = sb >= 0x7F80u;  // a NaN, an infinity or a range past fp32: all of the group reads as NaN
   sz = bad ? 0x7FFF7FFFu : (sb | ends << 16);
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f, half = 0.5f * s;
-  uint32_t codes = 0u;
+  const float s = __uint_as_float(sb << 16);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv *= 1.f - 0x1p-21f;  // 2^-23 off at most: now between (1 - 2^-20) / s and 1 / s
+  const int half = __float_as_int(0.5f * s);
+  const float magic = 12582912.f;  // 1.5 2^23: sums with it are integers, in their low bits
+  const uint64_t lo2f = f2_pack(lo, lo), inv2 = f2_pack(inv, inv), magic2 = f2_pack(magic, magic), minus = f2_pack(-s, -s);
+  uint32_t codes = 0u - 0x4B400000u * 0x11111111u;  // the bits of 1.5 2^23 in each term, taken out
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = (i & 1) ? hi_f(w[i / 2]) : lo_f(w[i / 2]);
-    const float t = __fsub_rn(x, lo);
-    // k = rint(t / s) but for the quotient's rounding: the integer in the low
-    // bits of a sum with 1.5 2^23. The remainder says whether it is off (a tie
-    // counts where k is odd). t / s <= 15 (1 + 2^-8), so k stays in 0..15.
-    const float kf = fmaf(t, inv, 12582912.f);
-    const int k = __float_as_int(kf);
-    const float r = fmaf(-(kf - 12582912.f), s, t);
-    const int one = (__float_as_int(r) >> 31) | 1;  // -1 or 1, where the remainder points
-    const bool off = fabsf(r) > __int_as_float(__float_as_int(half) - (k & 1));
-    codes |= static_cast<uint32_t>((k + (off ? one : 0)) & 15) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = f2_sub(f2_pack(lo_f(w[i]), hi_f(w[i])), lo2f);
+    const uint64_t kf = f2_fma(t, inv2, magic2);
+    const uint64_t r = f2_fma(f2_sub(kf, magic2), minus, t);
+    float k[2], rest[2];
+    f2_unpack(kf, k[0], k[1]);
+    f2_unpack(r, rest[0], rest[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // One more if the remainder is over s / 2, or just that and k odd. (t <= 15 s (1 + 2^-8): codes stay below 16.)
+      int c = __float_as_int(k[e]);
+      if (rest[e] > __int_as_float(half - (c & 1))) ++c;
+      codes += static_cast<uint32_t>(c) << (4 * (2 * i + e));
+    }
   }
-  return s > 0.f && !bad ? codes : 0u;
+  return sb != 0u && !bad ? codes : 0u;
 }
 
 }  // namespace
 
 // d/8 lanes own a row, 16 bytes each; a group of lanes takes up to R
 // consecutive heads of one token, all read before the first is written. The CTAs
-// of q come first, then those of k and of v.
+// of q, k and v take turns (`ratio` of q, one of k, one of v): those that
+// quantise are bound by their instructions, the others by HBM.
 template <int D, bool INTER, bool Q4, int R>
 __global__ void __launch_bounds__(256) fa_kv_append_kernel(const KvAppendArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR;
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
-  const int section = static_cast<int>(blockIdx.x) < a.q_ctas ? 0 : (static_cast<int>(blockIdx.x) < a.q_ctas + a.k_ctas ? 1 : 2);
-  const int cta = blockIdx.x - (section == 0 ? 0 : a.q_ctas + (section - 1) * a.k_ctas);
+  int section = 0, cta = blockIdx.x;
+  if (cta < a.k_ctas * (a.ratio + 2)) {
+    const int turn = cta / (a.ratio + 2), at = cta - turn * (a.ratio + 2);
+    section = max(at - a.ratio + 1, 0);
+    cta = section == 0 ? turn * a.ratio + at : turn;
+  } else {
+    cta -= 2 * a.k_ctas;  // the rest of q's
+  }
   const int slices = section == 0 ? a.q_slices : a.k_slices, heads = section == 0 ? a.H : a.Hk;
   const long long u = static_cast<long long>(cta) * GROUPS + threadIdx.x / LPR;
-  const long long token = min(u / slices, a.T - 1);
-  const int head0 = static_cast<int>(u % slices) * R;
+  long long token;
+  int head0;
+  if (a.T * slices <= 0x7fffffffLL) {  // a 64-bit division would take half as long as a row
+    const unsigned t = static_cast<unsigned>(u) / static_cast<unsigned>(slices);
+    token = t;
+    head0 = (static_cast<unsigned>(u) - t * slices) * R;
+  } else {
+    token = u / slices;
+    head0 = static_cast<int>(u - token * slices) * R;
+  }
+  token = min(token, a.T - 1);
   const int slot = section == 0 ? 0 : a.slots[token];
   // Slots outside the pool (negative ones mark padding) are not written.
   const bool live = u < a.T * slices && (section == 0 || (slot >= 0 && slot < a.num_blocks * a.block_size));
@@ -275,8 +302,8 @@ static cudaError_t launch_append_r(KvAppendArgs a, cudaStream_t stream) {
   auto ctas = [&](long long units) { return (units + kGroups - 1) / kGroups; };
   const long long q = a.H > 0 ? ctas(a.T * a.q_slices) : 0, k = ctas(a.T * a.k_slices);
   if (q + 2 * k > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  a.q_ctas = static_cast<int>(q);
   a.k_ctas = static_cast<int>(k);
+  a.ratio = static_cast<int>(q / k);
   auto kern = a.interleaved ? fa_kv_append_kernel<D, true, Q4, R> : fa_kv_append_kernel<D, false, Q4, R>;
   kern<<<static_cast<unsigned>(q + 2 * k), 256, 0, stream>>>(a);
   return cudaGetLastError();
