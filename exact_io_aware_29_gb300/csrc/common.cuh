@@ -295,7 +295,8 @@ struct Q4DecodeArgs {
   // The workspace: two parts (its first and its last item) of every CTA, and the items that CTAs cut.
   float* part_o;              // fp32 [2 kQ4MaxCtas][rows_per][D], normalised
   float* part_lse;            // fp32 [2 kQ4MaxCtas][rows_per], base 2
-  int4* cuts;                 // [kQ4MaxCtas]: (sequence or -1, item of it, part of the CTA before it, last CTA)
+  int4* cuts;                 // [kQ4MaxCtas]: (sequence or -1, item of it, first part, last CTA)
+  int cuts_by_item;           // set at launch: the cuts are told by item, not by the CTA of the first part
 };
 constexpr int kQ4Tile = 128;           // keys of a tile
 constexpr int kQ4Head = 3;             // an item's cost besides its tiles, in tiles

@@ -159,24 +159,41 @@ struct Q4Rows {
   float sum[NT][NG][2];      // scale log2e times the sum of the row's group
 };
 
+// The queries as they lie in memory: elements 64 g + 16 c + {0 .. 15} of row 8 j + r.
 template <int D, int NT>
-__device__ __forceinline__ void q4_load_rows(const Q4DecodeArgs& a, int b, int kvh, int row0, int rows, int lane,
-                                             Q4Rows<D, NT>& R) {
+struct Q4Raw {
+  uint4 x[NT][D / 64][2];
+  __device__ __forceinline__ void read(const Q4DecodeArgs& a, int b, int kvh, int row0, int rows, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const bool on = j * 8 + r < rows;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                        (on ? q4_row(a, b, kvh, row0 + j * 8 + r) : 0LL) * D);
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[j][g][h] = on ? src[g * 8 + c * 2 + h] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void q4_rows(const Q4DecodeArgs& a, const Q4Raw<D, NT>& raw, int lane, Q4Rows<D, NT>& R) {
   constexpr int NG = D / 64;
-  const int r = lane >> 2, c = lane & 3;
+  const int c = lane & 3;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const bool on = j * 8 + r < rows;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                      (on ? q4_row(a, b, kvh, row0 + j * 8 + r) : 0LL) * D);
-    uint32_t w[NG][8];  // elements 64 g + 16 c + {0 .. 15}
+    uint32_t w[NG][8];
     float mx = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const uint4 x = on ? src[g * 8 + c * 2] : make_uint4(0u, 0u, 0u, 0u);
-      const uint4 y = on ? src[g * 8 + c * 2 + 1] : make_uint4(0u, 0u, 0u, 0u);
-      w[g][0] = x.x, w[g][1] = x.y, w[g][2] = x.z, w[g][3] = x.w;
-      w[g][4] = y.x, w[g][5] = y.y, w[g][6] = y.z, w[g][7] = y.w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = raw.x[j][g][h];
+        w[g][4 * h] = x.x, w[g][4 * h + 1] = x.y, w[g][4 * h + 2] = x.z, w[g][4 * h + 3] = x.w;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(lo_f(w[g][i])), fabsf(hi_f(w[g][i]))));
     }
@@ -513,6 +530,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   int* found = reinterpret_cast<int*>(warp_sum + C::WARPS);  // sequence of the CTA's first tile, units of those before it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // launched programmatically: nothing of the stream's is read before
 
   // The tiles of all sequences (and, in the upper half, how many have any), and
   // the sequence that this CTA's run starts in: each thread adds up a stretch of
@@ -560,40 +578,54 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
   __syncthreads();
   Q4Walk w;
   w.left = 0;
-  int4 cut = make_int4(-1, 0, 0, 0);
+  const int run_end = shares.start(cta + 1);
   if (cta < ctas) {
     w.b = found[0];
     const int rem = start - found[1], u = q4_tiles(q4_len(a, w.b)) + head;
     w.item = rem / u;
     const int into = rem - w.item * u;  // units of the item in front of the run
     w.tile = max(into - head, 0);
-    w.left = shares.start(cta + 1) - start - max(head - into, 0);
+    w.left = run_end - start - max(head - into, 0);
     w.enter(a);
-    if (w.tile > 0) {
-      // For the kernel that joins: whether this CTA is the second one of a cut item.
-      const int first = start - into, prev = shares.of(start - 1), at = shares.start(prev);
-      if (at <= first + head) cut = make_int4(w.b, w.item, at >= first ? 0 : 1, shares.of(first + u - 1));
-    }
   }
-  if (threadIdx.x == 0) a.cuts[cta] = cut;
+  // For the kernel that joins: the item that begins in this run and does not end
+  // in it, by CTA (there is one at most) or by item.
+  if (threadIdx.x == 0 && !a.cuts_by_item) a.cuts[cta] = make_int4(-1, 0, 0, 0);
 
   if (w.left > 0) {
     const uint8_t* ring = smem + warp * (C::STAGES * C::STAGE_BYTES);
+    const int G = a.H / a.Hk;
+    int kvh, row0, rows;
+    auto item = [&]() {
+      kvh = w.item / a.row_blocks;
+      row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
+      rows = min(a.n_new * G - row0, C::ROWS);
+    };
+    item();
+    // The first item's queries are asked for in front of the copies, behind
+    // which they would wait (64 sequences of up to 8192 tokens: MEASURED2).
+    Q4Raw<D, NT> raw;
+    raw.read(a, w.b, kvh, row0, rows, lane);
     Q4Copies<D, NT> copies;
     copies.begin(a, w, head, smem_u32(ring), warp, lane);
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) copies.copy(a, s, warp, lane);
     const int r = lane >> 2, c = lane & 3;
-    const int G = a.H / a.Hk;
     float* red_o = reinterpret_cast<float*>(smem + C::OFF_RED);  // [warp][ROWS][RED_STRIDE]
     float* red_ml = reinterpret_cast<float*>(smem + C::OFF_ML);  // [warp][ROWS][2]
     int stage = 0;
     bool first_item = true;
     do {
-      const int kvh = w.item / a.row_blocks, row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
-      const int rows = min(a.n_new * G - row0, C::ROWS);
+      if (!first_item) {
+        item();
+        raw.read(a, w.b, kvh, row0, rows, lane);
+      }
+      if (threadIdx.x == 0 && w.tile == 0 && (a.cuts_by_item || w.here < w.n))
+        a.cuts[a.cuts_by_item ? w.b * items + w.item : cta] =
+            w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1), shares.of(run_end - w.left + w.n - 1))
+                         : make_int4(-1, 0, 0, 0);
       Q4Rows<D, NT> R;
-      q4_load_rows<D, NT>(a, w.b, kvh, row0, rows, lane, R);
+      q4_rows<D, NT>(a, raw, lane, R);
       Q4State<D, NT> S;
       S.clear();
       // Of the tile's keys of this warp: those in the sequence, and those that every row sees.
@@ -685,26 +717,30 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     for (int x = threadIdx.x; x < n * (D / 8); x += C::THREADS)
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + row * D)[x] = make_uint4(0u, 0u, 0u, 0u);
     for (int x = threadIdx.x; x < n; x += C::THREADS) a.lse[row + x] = -INFINITY;
+    for (int x = threadIdx.x; a.cuts_by_item && x < items; x += C::THREADS)
+      a.cuts[b * items + x] = make_int4(-1, 0, 0, 0);
   }
 }
 
-// Joins the parts of cut items: CTA (x, y) four rows (from 4 y on) of the item
-// whose second part is grid CTA x's first one. O = sum of 2^(lse_i - M) O_i over
-// the sum of the weights, in a fixed order: a row's four warps take every fourth
-// part, then the first adds up theirs. The first four parts of a warp are read
-// along with the sums: with up to 16 parts there are two reads to wait for.
-template <int D>
-__global__ void __launch_bounds__(512) fa_decode_q4_join_kernel(const Q4DecodeArgs a) {
-  constexpr int CPL = D / 32, SUBS = 4, AHEAD = 4;  // columns per lane
-  __shared__ float red[16][D + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % SUBS, x = blockIdx.y * 4 + warp / SUBS;
+// Joins the parts of cut items: CTA (x, y) rows of the x-th cut. O = sum of
+// 2^(lse_i - M) O_i over the sum of the weights, in a fixed order: a row's SUBS
+// warps take every SUBS-th part, then the first adds up theirs. A warp's first
+// eight parts are read along with the sums, so that with 8 SUBS parts there are
+// two reads to wait for.
+template <int D, int SUBS>
+__global__ void __launch_bounds__(512, 2) fa_decode_q4_join_kernel(const Q4DecodeArgs a) {
+  constexpr int CPL = D / 32, AHEAD = 8;  // columns per lane
+  __shared__ float red[SUBS > 1 ? 16 : 1][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % SUBS;
+  const int x = blockIdx.y * (blockDim.x / (32 * SUBS)) + warp / SUBS;
+  if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int4 cut = a.cuts[blockIdx.x];
   if (cut.x < 0) return;
   const int kvh = cut.y / a.row_blocks, row0 = (cut.y - kvh * a.row_blocks) * a.rows_per;
   const bool on = x < min(a.n_new * (a.H / a.Hk) - row0, a.rows_per);
-  const int c0 = blockIdx.x - 1, n = on ? cut.w - c0 + 1 : 0;
-  auto part = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? cut.z : 0)) * a.rows_per + x; };
+  const int n = on ? cut.w - cut.z / 2 + 1 : 0;
+  auto part = [&](int i) { return static_cast<size_t>(i == 0 ? cut.z : cut.z / 2 * 2 + 2 * i) * a.rows_per + x; };
   struct Part {
     float lse, y[CPL];
   };
@@ -744,10 +780,12 @@ __global__ void __launch_bounds__(512) fa_decode_q4_join_kernel(const Q4DecodeAr
 #pragma unroll 4
     for (int i = sub + AHEAD * SUBS; i < n; i += SUBS) add(read(i));
   }
+  if constexpr (SUBS > 1) {
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) red[warp][lane * CPL + k] = acc[k];
-  if (lane == 0) red[warp][D] = sum;
-  __syncthreads();
+    for (int k = 0; k < CPL; ++k) red[warp][lane * CPL + k] = acc[k];
+    if (lane == 0) red[warp][D] = sum;
+    __syncthreads();
+  }
   if (!on || sub > 0) return;
 #pragma unroll
   for (int v = 1; v < SUBS; ++v) {
@@ -764,20 +802,28 @@ __global__ void __launch_bounds__(512) fa_decode_q4_join_kernel(const Q4DecodeAr
 }
 
 template <int D, int NT>
-static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks) {
+static cudaError_t launch_q4_t(const Q4DecodeArgs& args, cudaStream_t stream, const LaunchMarks* marks) {
   using C = Q4Cfg<D, NT>;
+  Q4DecodeArgs a = args;
+  // Few items can have many parts each: eight warps to a row, a CTA per item.
+  // (One of 131072 tokens, 8 key heads: MEASURED3)
+  a.cuts_by_item = static_cast<long long>(a.B) * a.Hk * a.row_blocks <= C::CTAS * 152 / 16;
   auto kern = fa_decode_q4_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int grid = std::min(a.most_tiles, C::CTAS * 152);
   mark(marks, true, 0, stream);
-  kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_maybe_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, marks == nullptr, a);
   mark(marks, false, 0, stream);
   if (e != cudaSuccess) return e;
   mark(marks, true, 1, stream);
-  e = launch_maybe_pdl(fa_decode_q4_join_kernel<D>, dim3(grid, (std::min(a.n_new * (a.H / a.Hk), C::ROWS) + 3) / 4),
-                       dim3(512), 0, stream, marks == nullptr, a);
+  if (a.cuts_by_item) {
+    const unsigned rows = std::min(a.n_new * (a.H / a.Hk), C::ROWS);
+    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 8>, dim3(a.B * a.Hk * a.row_blocks, (rows + 1) / 2), dim3(512), 0,
+                         stream, marks == nullptr, a);
+  } else {
+    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 1>, dim3(grid), dim3(32 * C::ROWS), 0, stream, marks == nullptr, a);
+  }
   mark(marks, false, 1, stream);
   return e;
 }

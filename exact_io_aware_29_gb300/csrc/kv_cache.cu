@@ -154,6 +154,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[4], uint32_t& s
 template <int D, bool INTER, bool Q4, int R>
 __global__ void __launch_bounds__(256) fa_kv_append_kernel(const KvAppendArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR;
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // launched programmatically: nothing of the stream's is read or written before
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
   int section = 0, cta = blockIdx.x;
   if (cta < a.k_ctas * (a.ratio + 2)) {
@@ -238,6 +240,8 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_kv_gather_q4_kernel(const KvGatherArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR, R = 4;
   __shared__ long long place[kGatherTokens];  // row of head 0 in the cache; -1: reads as zeros; -2: of no sequence
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // as above
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = threadIdx.x % LPR;
   const int row0 = blockIdx.x * a.tokens, count = min(a.tokens, a.total - row0);
   for (int t = warp; t < count; t += 8) {
@@ -305,8 +309,7 @@ static cudaError_t launch_append_r(KvAppendArgs a, cudaStream_t stream) {
   a.k_ctas = static_cast<int>(k);
   a.ratio = static_cast<int>(q / k);
   auto kern = a.interleaved ? fa_kv_append_kernel<D, true, Q4, R> : fa_kv_append_kernel<D, false, Q4, R>;
-  kern<<<static_cast<unsigned>(q + 2 * k), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_maybe_pdl(kern, dim3(static_cast<unsigned>(q + 2 * k)), dim3(256), 0, stream, true, a);
 }
 
 template <int D, bool Q4>
@@ -325,9 +328,8 @@ cudaError_t launch_kv_gather_q4(const KvGatherArgs& args, cudaStream_t stream) {
   KvGatherArgs a = args;
   a.tokens = std::min(std::max(a.total / (152 * 4), 1), kGatherTokens);
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.total) + a.tokens - 1) / a.tokens);
-  if (a.D == 64) fa_kv_gather_q4_kernel<64><<<grid, 256, 0, stream>>>(a);
-  else fa_kv_gather_q4_kernel<128><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_maybe_pdl(a.D == 64 ? fa_kv_gather_q4_kernel<64> : fa_kv_gather_q4_kernel<128>, dim3(grid), dim3(256),
+                          0, stream, true, a);
 }
 
 }  // namespace fa
