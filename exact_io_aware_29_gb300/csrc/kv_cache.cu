@@ -152,10 +152,12 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[4], uint32_t& s
 // of q, k and v take turns (`ratio` of q, one of k, one of v): those that
 // quantise are bound by their instructions, the others by HBM.
 template <int D, bool INTER, bool Q4, int R>
-__global__ void __launch_bounds__(256) fa_kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(256, R == 8 ? 4 : 5) fa_kv_append_kernel(const KvAppendArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR;
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  griddep_wait();  // launched programmatically: nothing of the stream's is read or written before
+  // Launched programmatically: nothing of the stream's is read or written before
+  // this. (What follows is not let in early: CTAs that only wait would take room.
+  // 16384 tokens written and read back: 94 us if it is, 89 as it stands.)
+  griddep_wait();
   const int lane = threadIdx.x & 31, l = threadIdx.x % LPR;
   int section = 0, cta = blockIdx.x;
   if (cta < a.k_ctas * (a.ratio + 2)) {
@@ -235,12 +237,13 @@ __device__ __forceinline__ int count_upto(const int* cu, int n, int row, int lan
 // codes are exact, 128 + code being the bits of a nibble under 128's exponent).
 // A CTA takes `tokens` packed rows: its warps look up where they lie, then
 // groups of d/8 lanes take a token's K or V each, four heads at a time.
-constexpr int kGatherTokens = 32;
+// (110000 tokens of 8 heads, d 128: 75.4 us with 8 rows a CTA, 77.4 with 4, 78.2
+// with 16, 81.8 with 32; eight heads at a time 77.8.)
+constexpr int kGatherTokens = 8;
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv_gather_q4_kernel(const KvGatherArgs a) {
   constexpr int LPR = D / 8, GROUPS = 256 / LPR, R = 4;
   __shared__ long long place[kGatherTokens];  // row of head 0 in the cache; -1: reads as zeros; -2: of no sequence
-  if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();  // as above
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = threadIdx.x % LPR;
   const int row0 = blockIdx.x * a.tokens, count = min(a.tokens, a.total - row0);
@@ -314,9 +317,14 @@ static cudaError_t launch_append_r(KvAppendArgs a, cudaStream_t stream) {
 
 template <int D, bool Q4>
 static cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
-  // Four rows to a group of lanes once that leaves two CTAs or more for every SM.
-  return a.T * (a.H + 2 * a.Hk) * (D / 8) >= 152LL * 2 * 256 * 4 ? launch_append_r<D, Q4, 4>(a, stream)
-                                                                 : launch_append_r<D, Q4, 1>(a, stream);
+  // Four rows to a group of lanes once that leaves two CTAs for every SM, and
+  // eight of those that are quantised where there are many. (16384 tokens, d 128,
+  // with one, two, four and eight rows: 32 + 8 heads 111, 78, 61 and 61 us in
+  // bf16; written in 4 bits and read back, 138, 115, 82 and 78 us, 16 + 4 heads
+  // 73, 61, 46 and 50; 512 tokens of those 5.9, 5.8, 6.7 and 6.8.)
+  const long long lanes = a.T * (a.H + 2 * a.Hk) * (D / 8);
+  if (Q4 && D == 128 && a.Hk >= 8 && lanes >= 152LL * 4 * 256 * 8) return launch_append_r<D, Q4, 8>(a, stream);
+  return lanes >= 152LL * 2 * 256 * 4 ? launch_append_r<D, Q4, 4>(a, stream) : launch_append_r<D, Q4, 1>(a, stream);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
