@@ -66,8 +66,7 @@ namespace {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -279,24 +278,38 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
   const int ka = (r >> 1) + 4 * (r & 1);
   float sc[NT][KH][2];  // [key ka + 8 h][row i]
   uint32_t vsz[NG][KH];
+  float acc[C::HALVES][NT][NG][4];
+  {
+    uint2 x[C::HALVES][NG], y[C::HALVES][NG];
 #pragma unroll
-  for (int s = 0; s < C::HALVES; ++s) {
-    float acc[NT][NG][4];
+    for (int s = 0; s < C::HALVES; ++s) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint2 x = *reinterpret_cast<const uint2*>(st + (ka + 16 * s) * (D / 2) + g * 32 + c * 8);
-      const uint2 y = *reinterpret_cast<const uint2*>(st + (ka + 16 * s + 8) * (D / 2) + g * 32 + c * 8);
-      const uint32_t wx[4] = {x.x, x.x >> 8, x.y, x.y >> 8}, wy[4] = {y.x, y.x >> 8, y.y, y.y >> 8};
+      for (int g = 0; g < NG; ++g) {
+        x[s][g] = *reinterpret_cast<const uint2*>(st + (ka + 16 * s) * (D / 2) + g * 32 + c * 8);
+        y[s][g] = *reinterpret_cast<const uint2*>(st + (ka + 16 * s + 8) * (D / 2) + g * 32 + c * 8);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j][g][0] = acc[j][g][1] = acc[j][g][2] = acc[j][g][3] = 0.f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          mma_f16(acc[j][g], wx[t] & 0x000F000Fu, wy[t] & 0x000F000Fu, wx[t] & 0x00F000F0u, wy[t] & 0x00F000F0u,
-                  R.q[j][g][t][0], R.q[j][g][t][1]);
+        for (int j = 0; j < NT; ++j) acc[s][j][g][0] = acc[s][j][g][1] = acc[s][j][g][2] = acc[s][j][g][3] = 0.f;
       }
     }
+    // Products that do not wait for one another in a row.
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int s = 0; s < C::HALVES; ++s) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t wx = (t < 2 ? x[s][g].x : x[s][g].y) >> (8 * (t & 1));
+          const uint32_t wy = (t < 2 ? y[s][g].x : y[s][g].y) >> (8 * (t & 1));
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma_f16(acc[s][j][g], wx & 0x000F000Fu, wy & 0x000F000Fu, wx & 0x00F000F0u, wy & 0x00F000F0u,
+                    R.q[j][g][t][0], R.q[j][g][t][1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < C::HALVES; ++s) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int h = 2 * s + e;
@@ -318,10 +331,10 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = acc[j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
+          float x = acc[s][j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
 #pragma unroll
           for (int g = 1; g < NG; ++g) {
-            x = fmaf(acc[j][g][2 * e + i], lo_f(ksz[g]), x);
+            x = fmaf(acc[s][j][g][2 * e + i], lo_f(ksz[g]), x);
             y = fmaf(hi_f(ksz[g]), R.sum[j][g][i], y);
           }
           sc[j][h][i] = fmaf(x, R.qs[j][i], y);
@@ -804,6 +817,7 @@ __global__ void __launch_bounds__(512, 2) fa_decode_q4_join_kernel(const Q4Decod
 template <int D, int NT>
 static cudaError_t launch_q4_t(const Q4DecodeArgs& args, cudaStream_t stream, const LaunchMarks* marks) {
   using C = Q4Cfg<D, NT>;
+  static_assert(C::CTAS * 152 <= kQ4MaxCtas, "the workspace holds every CTA's parts");
   Q4DecodeArgs a = args;
   // Few items can have many parts each: eight warps to a row, a CTA per item.
   // (One of 131072 tokens, 8 key heads: MEASURED3)
