@@ -1337,6 +1337,15 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
     return FA_ERR_UNSUPPORTED;
   a->row_blocks = static_cast<int>(blocks);
   a->most_tiles = static_cast<int>(tiles * B * H_kv * blocks);
+  const long long items = blocks * B * H_kv, ctas = fa::q4_ctas(d, a->rows_per) * 152;
+  // A cluster for each item where all of them run at once and no CTA has more
+  // than SPREADMAX tiles. (MEASURED4)
+  a->spread = items * fa::kQ4Cluster <= ctas && tiles <= fa::kQ4Cluster * 4;
+  // Few items can have many parts each: then eight warps join a row, a CTA two
+  // rows of an item. (One sequence of 131072 tokens, 8 key heads, 57 parts each:
+  // 33.7 us, 38.1 with the joins by CTA; four of up to 1200, 4 key heads, 10
+  // parts: 9.7 and 9.0.)
+  a->cuts_by_item = std::min<long long>(a->most_tiles, ctas) / items >= 32;
   return FA_OK;
 }
 
@@ -1396,7 +1405,7 @@ int fa_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.o);
   a.cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.o + ws.lse);
   fa::LaunchMarks marks;
-  const bool timed = next_marks(&marks, 4, 2);
+  const bool timed = next_marks(&marks, 4, a.spread ? 1 : 2);
   cudaError_t e = fa::launch_decode_q4(a, s, timed ? &marks : nullptr);
   if (e != cudaSuccess) return launch_error(e);
   if (check_mode()) return fa_check_status(stream);

@@ -33,6 +33,9 @@
 // an item ends.
 // Softmax statistics and sums are fp32. A cut item's parts are joined in the
 // order of the keys by a second kernel.
+// A step of few, short sequences goes another way, its time being a sum of
+// latencies: a cluster of eight CTAs shares an item's tiles and joins its parts
+// through their shared memory.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -48,7 +51,7 @@ struct Q4Cfg {
   static constexpr int HALVES = KEYS / 16;
   static constexpr int WARPS = kQ4Tile / KEYS;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NT - 1);  // per SM (registers: 168, 128 at d 64 with NT = 1)
+  static constexpr int CTAS = q4_ctas(D, ROWS);    // per SM (registers: 168, 128 at d 64 with NT = 1)
   // A stage of a warp's ring: codes of K and V, scales of K and V.
   static constexpr int CODE_BYTES = KEYS * D / 2, SCALE_BYTES = KEYS * NG * 4;
   static constexpr int OFF_VC = CODE_BYTES, OFF_KS = 2 * CODE_BYTES, OFF_VS = OFF_KS + SCALE_BYTES;
@@ -534,17 +537,17 @@ struct Q4Copies {
 
 }  // namespace
 
+// Where a CTA's run begins, and what it needs to say where its last item ends.
+struct Q4Start {
+  Q4Walk w;
+  int head, run_end;
+  Q4Shares shares;
+};
 template <int D, int NT>
-__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_decode_q4_kernel(const Q4DecodeArgs a) {
+__device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem, int warp, int lane) {
   using C = Q4Cfg<D, NT>;
-  constexpr int NG = C::NG;
-  extern __shared__ __align__(128) uint8_t smem[];
   long long* warp_sum = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
   int* found = reinterpret_cast<int*>(warp_sum + C::WARPS);  // sequence of the CTA's first tile, units of those before it
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  griddep_wait();  // launched programmatically: nothing of the stream's is read before
-
   // The tiles of all sequences (and, in the upper half, how many have any), and
   // the sequence that this CTA's run starts in: each thread adds up a stretch of
   // sequences, then their sums are scanned.
@@ -570,9 +573,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     if (v < warp) before += warp_sum[v];
     all += warp_sum[v];
   }
-  // An item costs about two tiles' time besides its tiles (its queries, and the
-  // join of the warps). Where runs are short, what counts is the longest of
-  // them: only tiles then. (64 sequences of up to 8192 tokens: MEASURED)
+  // An item costs about three tiles' time besides its tiles (its queries, the
+  // first steps' maxima, the join of the warps): 64 sequences of up to 8192
+  // tokens 65.5 us, 71.7 if it is left out. Where runs are short, what counts is
+  // the longest of them: only tiles then.
   const int tiles = static_cast<int>(all) * items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
   const int head = tiles >= 8 * ctas ? kQ4Head : 0;
@@ -589,36 +593,61 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     found[0] = b, found[1] = x;
   }
   __syncthreads();
-  Q4Walk w;
-  w.left = 0;
-  const int run_end = shares.start(cta + 1);
+  Q4Start at{Q4Walk{}, head, shares.start(cta + 1), shares};
   if (cta < ctas) {
+    Q4Walk& w = at.w;
     w.b = found[0];
     const int rem = start - found[1], u = q4_tiles(q4_len(a, w.b)) + head;
     w.item = rem / u;
     const int into = rem - w.item * u;  // units of the item in front of the run
     w.tile = max(into - head, 0);
-    w.left = run_end - start - max(head - into, 0);
+    w.left = at.run_end - start - max(head - into, 0);
     w.enter(a);
   }
+  return at;
+}
+// The same for an item shared by a cluster: its tiles in equal runs.
+template <int D, int NT>
+__device__ __forceinline__ Q4Start q4_start_spread(const Q4DecodeArgs& a) {
+  Q4Start at{Q4Walk{}, 0, 0, Q4Shares(0, 1, 0)};
+  const int items = a.Hk * a.row_blocks, id = blockIdx.x / kQ4Cluster, rank = blockIdx.x % kQ4Cluster;
+  Q4Walk& w = at.w;
+  w.b = id / items;
+  w.item = id - w.b * items;
+  const int n = q4_tiles(q4_len(a, w.b));
+  w.tile = rank * n / kQ4Cluster;
+  w.left = (rank + 1) * n / kQ4Cluster - w.tile;
+  w.enter(a);
+  return at;
+}
+
+template <int D, int NT, bool SPREAD>
+__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_decode_q4_kernel(const Q4DecodeArgs a) {
+  using C = Q4Cfg<D, NT>;
+  constexpr int NG = C::NG;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!SPREAD && threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // launched programmatically: nothing of the stream's is read before
+  const int items = a.Hk * a.row_blocks, cta = blockIdx.x, G = a.H / a.Hk;
+  Q4Start at = SPREAD ? q4_start_spread<D, NT>(a) : q4_start<D, NT>(a, smem, warp, lane);
+  Q4Walk& w = at.w;
+  const int head = at.head;
+  int kvh, row0, rows;
+  auto item = [&]() {
+    kvh = w.item / a.row_blocks;
+    row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
+    rows = min(a.n_new * G - row0, C::ROWS);
+  };
   // For the kernel that joins: the item that begins in this run and does not end
   // in it, by CTA (there is one at most) or by item.
-  if (threadIdx.x == 0 && !a.cuts_by_item) a.cuts[cta] = make_int4(-1, 0, 0, 0);
+  if (!SPREAD && threadIdx.x == 0 && !a.cuts_by_item) a.cuts[cta] = make_int4(-1, 0, 0, 0);
+  // A cluster's parts: this CTA's, [ROWS][RED_STRIDE], a row's maximum and sum
+  // behind its columns.
+  float* share = reinterpret_cast<float*>(smem);
 
   if (w.left > 0) {
     const uint8_t* ring = smem + warp * (C::STAGES * C::STAGE_BYTES);
-    const int G = a.H / a.Hk;
-    int kvh, row0, rows;
-    auto item = [&]() {
-      kvh = w.item / a.row_blocks;
-      row0 = (w.item - kvh * a.row_blocks) * C::ROWS;
-      rows = min(a.n_new * G - row0, C::ROWS);
-    };
-    item();
-    // The first item's queries are asked for in front of the copies, behind
-    // which they would wait (64 sequences of up to 8192 tokens: MEASURED2).
-    Q4Raw<D, NT> raw;
-    raw.read(a, w.b, kvh, row0, rows, lane);
     Q4Copies<D, NT> copies;
     copies.begin(a, w, head, smem_u32(ring), warp, lane);
 #pragma unroll
@@ -629,13 +658,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     int stage = 0;
     bool first_item = true;
     do {
-      if (!first_item) {
-        item();
-        raw.read(a, w.b, kvh, row0, rows, lane);
-      }
-      if (threadIdx.x == 0 && w.tile == 0 && (a.cuts_by_item || w.here < w.n))
+      item();
+      Q4Raw<D, NT> raw;
+      raw.read(a, w.b, kvh, row0, rows, lane);
+      if (!SPREAD && threadIdx.x == 0 && w.tile == 0 && (a.cuts_by_item || w.here < w.n))
         a.cuts[a.cuts_by_item ? w.b * items + w.item : cta] =
-            w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1), shares.of(run_end - w.left + w.n - 1))
+            w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1), at.shares.of(at.run_end - w.left + w.n - 1))
                          : make_int4(-1, 0, 0, 0);
       Q4Rows<D, NT> R;
       q4_rows<D, NT>(a, raw, lane, R);
@@ -676,11 +704,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float f = inverse_pow2(S.up[j][g][i]);
-            const float f0 = f * 0x1p24f, f1 = f * 0x1p20f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
               *reinterpret_cast<float2*>(&red_o[row * C::RED_STRIDE + g * 64 + r * 8 + t * 2]) =
-                  make_float2(fmaf(S.o[j][g][t][i], f0, S.z[j][g][i]), fmaf(S.o[j][g][t][2 + i], f1, S.z[j][g][i]));
+                  make_float2(fmaf(S.o[j][g][t][i] * 0x1p24f, f, S.z[j][g][i]),
+                              fmaf(S.o[j][g][t][2 + i] * 0x1p20f, f, S.z[j][g][i]));
           }
           if (r == 0) *reinterpret_cast<float2*>(&red_ml[row * 2]) = make_float2(S.m[j][i], S.l[j][i]);
         }
@@ -704,6 +732,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
           acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
           acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
         }
+        if constexpr (SPREAD) {  // (the rings have been read)
+          *reinterpret_cast<float4*>(&share[x * C::RED_STRIDE + col]) = acc;
+          if (col == 0) *reinterpret_cast<float2*>(&share[x * C::RED_STRIDE + D]) = make_float2(M, sum);
+          continue;
+        }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const float lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
         if (whole) {
@@ -721,6 +754,47 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
       first_item = false;
     } while (w.next(a, head));
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  if constexpr (SPREAD) {
+    // The cluster's parts, in the order of the keys: four columns of a row a
+    // thread, spread over all CTAs. A CTA without tiles has a sum of zero.
+    item();
+    if (w.here == 0) {
+      for (int x = threadIdx.x; x < rows; x += C::THREADS)
+        *reinterpret_cast<float2*>(&share[x * C::RED_STRIDE + D]) = make_float2(kNoLogit, 0.f);
+    }
+    cluster_sync();
+    const int rank = cta % kQ4Cluster;
+    for (int e = threadIdx.x * kQ4Cluster + rank; e < rows * (D / 4); e += C::THREADS * kQ4Cluster) {
+      const int x = e / (D / 4), col = e % (D / 4) * 4;
+      const uint32_t row = smem_u32(&share[x * C::RED_STRIDE]);
+      float4 ml[kQ4Cluster], y[kQ4Cluster];
+#pragma unroll
+      for (int v = 0; v < kQ4Cluster; ++v) {
+        const uint32_t from = map_to_rank(row, v);
+        ml[v] = ld_cluster_f4(from + D * 4);  // maximum, sum, nothing
+        y[v] = ld_cluster_f4(from + col * 4);
+      }
+      float M = kNoLogit, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < kQ4Cluster; ++v) M = fmaxf(M, ml[v].x);
+#pragma unroll
+      for (int v = 0; v < kQ4Cluster; ++v) {
+        if (ml[v].y == 0.f) continue;
+        const float f = ex2(ml[v].x - M);
+        sum = fmaf(ml[v].y, f, sum);
+        acc.x = fmaf(y[v].x, f, acc.x), acc.y = fmaf(y[v].y, f, acc.y);
+        acc.z = fmaf(y[v].z, f, acc.z), acc.w = fmaf(y[v].w, f, acc.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long to = q4_row(a, w.b, kvh, row0 + x);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + to * D + col) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (col == 0) a.lse[to] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // no CTA's shared memory goes before it has been read
+    return;
   }
   // Sequences without keys have no tiles: every CTA writes its share of their rows.
   for (int b = cta; b < a.B; b += gridDim.x) {
@@ -815,26 +889,24 @@ __global__ void __launch_bounds__(512, 2) fa_decode_q4_join_kernel(const Q4Decod
 }
 
 template <int D, int NT>
-static cudaError_t launch_q4_t(const Q4DecodeArgs& args, cudaStream_t stream, const LaunchMarks* marks) {
+static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks) {
   using C = Q4Cfg<D, NT>;
   static_assert(C::CTAS * 152 <= kQ4MaxCtas, "the workspace holds every CTA's parts");
-  Q4DecodeArgs a = args;
-  // Few items can have many parts each: eight warps to a row, a CTA per item.
-  // (One of 131072 tokens, 8 key heads: MEASURED3)
-  a.cuts_by_item = static_cast<long long>(a.B) * a.Hk * a.row_blocks <= C::CTAS * 152 / 16;
-  auto kern = fa_decode_q4_kernel<D, NT>;
+  auto kern = a.spread ? fa_decode_q4_kernel<D, NT, true> : fa_decode_q4_kernel<D, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(a.most_tiles, C::CTAS * 152);
+  const int items = a.B * a.Hk * a.row_blocks;
+  const int grid = a.spread ? items * kQ4Cluster : std::min(a.most_tiles, C::CTAS * 152);
   mark(marks, true, 0, stream);
-  e = launch_maybe_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, marks == nullptr, a);
+  e = launch_cluster_maybe_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, marks == nullptr,
+                               a.spread ? kQ4Cluster : 1, a);
   mark(marks, false, 0, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.spread) return e;
   mark(marks, true, 1, stream);
   if (a.cuts_by_item) {
     const unsigned rows = std::min(a.n_new * (a.H / a.Hk), C::ROWS);
-    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 8>, dim3(a.B * a.Hk * a.row_blocks, (rows + 1) / 2), dim3(512), 0,
-                         stream, marks == nullptr, a);
+    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 8>, dim3(items, (rows + 1) / 2), dim3(512), 0, stream,
+                         marks == nullptr, a);
   } else {
     e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 1>, dim3(grid), dim3(32 * C::ROWS), 0, stream, marks == nullptr, a);
   }

@@ -35,13 +35,14 @@ def _lib():
 class Step:
     """A seeded step: pages scattered over the pool, garbage (NaN scales among
     it) in every slot that no sequence owns, table entries past the last page
-    out of range."""
+    out of range. bound: the max_seq_len that is passed, if more than the
+    longest; one of 6000 keeps every step off the clusters' way."""
 
-    def __init__(self, lens, n_new, H, Hk, d, page, seed, q_scale=1.0, mul=1.0):
+    def __init__(self, lens, n_new, H, Hk, d, page, seed, q_scale=1.0, mul=1.0, bound=0):
         import torch
         rng = np.random.default_rng(seed)
         self.lens, self.n, self.H, self.Hk, self.d, self.page = np.asarray(lens, np.int32), n_new, H, Hk, d, page
-        self.B, self.max_len = len(lens), max(max(lens), 1)
+        self.B, self.max_len = len(lens), max(max(lens), bound, 1)
         pages = [-(-n // page) for n in lens]
         pool = sum(pages) + 2
         order = rng.permutation(pool).astype(np.int32)
@@ -136,10 +137,11 @@ CASES = [
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_against_oracle(d, case):
+@pytest.mark.parametrize("bound", [0, 6000])
+def test_against_oracle(d, case, bound):
     import torch
     lens, n, H, Hk, page = CASES[case]
-    x = Step(lens, n, H, Hk, d, page, 8100 + 10 * case + d)
+    x = Step(lens, n, H, Hk, d, page, 8100 + 10 * case + d, bound=bound)
     o, lse = x.run()
     x.check(o, lse)
     again = x.run()
@@ -158,9 +160,10 @@ def test_one_query_without_its_axis(d):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("mul", [2.0 ** 60, 2.0 ** -60])
-def test_values_of_any_range(mul):
-    x = Step([500, 40, 0], 2, 8, 2, 128, 64, 8310, mul=mul)
+@pytest.mark.parametrize("bound", [0, 6000])
+@pytest.mark.parametrize("mul", [2.0 ** 60, 2.0 ** -60, 2.0 ** 120, 2.0 ** -115])
+def test_values_of_any_range(mul, bound):
+    x = Step([500, 40, 0], 2, 8, 2, 128, 64, 8310, mul=mul, bound=bound)
     x.check(*x.run())
 
 
@@ -176,18 +179,19 @@ def test_queries_of_any_range(q_scale):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
-def test_nan_reaches_the_rows_that_see_it_and_no_other(d):
+@pytest.mark.parametrize("bound", [0, 6000])
+def test_nan_reaches_the_rows_that_see_it_and_no_other(d, bound):
     """A key or value group that reads as NaN: NaN in the rows that see the
     token (all of O and the LSE for a key, the group's elements for a value),
     the same bits as before in all others: other key heads, other sequences,
     queries before the token."""
     import torch
     lens, n, H, Hk, page = [200, 77, 5], 4, 6, 2, 32
-    x = Step(lens, n, H, Hk, d, page, 8400 + d)
+    x = Step(lens, n, H, Hk, d, page, 8400 + d, bound=bound)
     o, lse = x.run()
     for which in (1, 3):
         for b, t in ((0, 50), (0, 197), (0, 199), (1, 76), (2, 1)):
-            y = Step(lens, n, H, Hk, d, page, 8400 + d)
+            y = Step(lens, n, H, Hk, d, page, 8400 + d, bound=bound)
             y.cache[which][int(y.table[b, t // page]), 1, t % page, 0] = NAN
             o1, l1 = y.run()
             first = max(0, t - lens[b] + n)  # queries from here on see the token
@@ -202,8 +206,9 @@ def test_nan_reaches_the_rows_that_see_it_and_no_other(d):
 
 
 @pytest.mark.gpu
-def test_blocks_outside_the_pool_read_as_zeros():
-    x = Step([256, 130, 0, 64], 2, 8, 2, 128, 16, 8500)
+@pytest.mark.parametrize("bound", [0, 6000])
+def test_blocks_outside_the_pool_read_as_zeros(bound):
+    x = Step([256, 130, 0, 64], 2, 8, 2, 128, 16, 8500, bound=bound)
     for b, p, bad in ((0, 1, x.cache[0].shape[0]), (1, 0, -1), (0, 9, 2 ** 31 - 1), (3, 3, -2 ** 31)):
         x.table[b, p] = bad
         for v in x.values:
@@ -250,16 +255,12 @@ def test_pool_past_2_32_bytes():
 
 
 @pytest.mark.gpu
-def test_captured_and_on_two_streams():
+@pytest.mark.parametrize("bound", [900, 6000])
+def test_captured_and_on_two_streams(bound):
     """A captured step replayed on new queries, lengths and tables, while
     another step runs eagerly on a second stream with its own workspace."""
     import torch
-    xs = [Step([m, 40, 0, 129], 2, 8, 2, 128, 64, 8600 + m) for m in (900, 350)]
-    for x in xs:
-        x.max_len = 900
-        wide = np.full((4, 15), -7, np.int32)
-        wide[:, :x.table.shape[1]] = x.table
-        x.table = wide
+    xs = [Step([m, 40, 0, 129], 2, 8, 2, 128, 64, 8600 + m, bound=bound) for m in (900, 350)]
     other = Step([i for i in range(40)], 1, 16, 2, 64, 64, 8650)
     want, want_other = [x.run() for x in xs], other.run()
     pool = max(x.cache[0].shape[0] for x in xs)
@@ -267,7 +268,7 @@ def test_captured_and_on_two_streams():
     for i in range(1, 5):
         bufs[i] = torch.zeros((pool, *bufs[i].shape[1:]), dtype=bufs[i].dtype, device="cuda")
     o, lse = torch.empty_like(bufs[0]), torch.empty(4, 2, 8, device="cuda")
-    ws = torch.empty(binding.fa_decode_paged_q4_workspace_size(4, 2, 8, 2, 128, 900), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(binding.fa_decode_paged_q4_workspace_size(4, 2, 8, 2, 128, bound), dtype=torch.uint8, device="cuda")
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     step = lambda: binding.fa_decode_paged_q4(*bufs[:5], o, lse, *bufs[5:], ws, s1)  # noqa: E731
     torch.cuda.synchronize()
