@@ -1338,9 +1338,18 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   a->row_blocks = static_cast<int>(blocks);
   a->most_tiles = static_cast<int>(tiles * B * H_kv * blocks);
   const long long items = blocks * B * H_kv, ctas = fa::q4_ctas(d, a->rows_per) * 152;
-  // A cluster for each item where all of them run at once and no CTA has more
-  // than SPREADMAX tiles. (MEASURED4)
-  a->spread = items * fa::kQ4Cluster <= ctas && tiles <= fa::kQ4Cluster * 4;
+  // A cluster for each item, as many CTAs as leave room for all clusters at once
+  // and have a tile each, unless a CTA would have many tiles to go through, or
+  // more than the shares of an even split. (32/8 heads, d 128, in us, split evenly
+  // and in clusters of 8, 4, 2 and 1: one sequence of 1000 tokens 8.0, 7.0, 7.4,
+  // 8.6; 8 of 3000 15.9, 18.6, 12.2, 14.4; 16 of 3000 24.2, 31, 26, 18.5, 21.8; 48
+  // of 1000 23.1, -, -, 24.8, 18.3; 256 of 1000 72.2, -, -, 99, 70.7. One of 30000
+  // 17.9, 25.3; one of 8000 with one key head 8.8, 10.8; 16 of 8000 34.3, 46, 39,
+  // 35.6; 80 of 3000 58.9, -, -, 63, 61.)
+  int cs = fa::kQ4Cluster;
+  while (cs > 1 && (items * cs > ctas || cs / 2 >= tiles)) cs /= 2;
+  const int most = cs == 1 ? 8 : (items * cs * 2 > ctas ? 16 : (items >= 8 ? 8 : 6));
+  a->spread = (tiles + cs - 1) / cs <= most ? cs : 0;
   // Few items can have many parts each: then eight warps join a row, a CTA two
   // rows of an item. (One sequence of 131072 tokens, 8 key heads, 57 parts each:
   // 33.7 us, 38.1 with the joins by CTA; four of up to 1200, 4 key heads, 10

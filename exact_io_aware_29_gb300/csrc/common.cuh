@@ -291,7 +291,7 @@ struct Q4DecodeArgs {
   int block_size, num_blocks, max_blocks, max_seq_len;
   int row_blocks, rows_per;   // blocks of rows_per rows (row = query * G + head) of each sequence and key head
   int most_tiles;             // no more tiles in all than this
-  int spread;                 // 1: a cluster for each item, no parts and no second kernel
+  int spread;                 // CTAs of the cluster that an item has to itself (no parts, no second kernel), or 0
   int cuts_by_item;           // 1: the cuts are told by item, 0: by the CTA that has the first part
   float scale_log2;           // scale * log2(e)
   // The workspace: two parts (its first and its last item) of every CTA, and the items that CTAs cut.
@@ -301,7 +301,7 @@ struct Q4DecodeArgs {
 };
 constexpr int kQ4Tile = 128;           // keys of a tile
 constexpr int kQ4Head = 3;             // an item's cost besides its tiles, in tiles
-constexpr int kQ4Cluster = 8;          // CTAs of a cluster
+constexpr int kQ4Cluster = 8;          // most CTAs of a cluster
 constexpr int q4_ctas(int D, int rows_per) { return (D == 64 ? 4 : 3) - (rows_per > 8 ? 1 : 0); }  // CTAs per SM
 constexpr int kQ4MaxCtas = 4 * 152;
 cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks);

@@ -34,7 +34,7 @@
 // Softmax statistics and sums are fp32. A cut item's parts are joined in the
 // order of the keys by a second kernel.
 // A step of few, short sequences goes another way, its time being a sum of
-// latencies: a cluster of eight CTAs shares an item's tiles and joins its parts
+// latencies: a cluster of up to eight CTAs shares an item's tiles and joins its parts
 // through their shared memory.
 #include <cuda_bf16.h>
 
@@ -610,13 +610,13 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
 template <int D, int NT>
 __device__ __forceinline__ Q4Start q4_start_spread(const Q4DecodeArgs& a) {
   Q4Start at{Q4Walk{}, 0, 0, Q4Shares(0, 1, 0)};
-  const int items = a.Hk * a.row_blocks, id = blockIdx.x / kQ4Cluster, rank = blockIdx.x % kQ4Cluster;
+  const int items = a.Hk * a.row_blocks, id = blockIdx.x / a.spread, rank = blockIdx.x - id * a.spread;
   Q4Walk& w = at.w;
   w.b = id / items;
   w.item = id - w.b * items;
   const int n = q4_tiles(q4_len(a, w.b));
-  w.tile = rank * n / kQ4Cluster;
-  w.left = (rank + 1) * n / kQ4Cluster - w.tile;
+  w.tile = rank * n / a.spread;
+  w.left = (rank + 1) * n / a.spread - w.tile;
   w.enter(a);
   return at;
 }
@@ -764,13 +764,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
         *reinterpret_cast<float2*>(&share[x * C::RED_STRIDE + D]) = make_float2(kNoLogit, 0.f);
     }
     cluster_sync();
-    const int rank = cta % kQ4Cluster;
-    for (int e = threadIdx.x * kQ4Cluster + rank; e < rows * (D / 4); e += C::THREADS * kQ4Cluster) {
+    for (int e = threadIdx.x * a.spread + cta % a.spread; e < rows * (D / 4); e += C::THREADS * a.spread) {
       const int x = e / (D / 4), col = e % (D / 4) * 4;
       const uint32_t row = smem_u32(&share[x * C::RED_STRIDE]);
       float4 ml[kQ4Cluster], y[kQ4Cluster];
 #pragma unroll
       for (int v = 0; v < kQ4Cluster; ++v) {
+        ml[v].y = 0.f;
+        if (v >= a.spread) continue;
         const uint32_t from = map_to_rank(row, v);
         ml[v] = ld_cluster_f4(from + D * 4);  // maximum, sum, nothing
         y[v] = ld_cluster_f4(from + col * 4);
@@ -778,7 +779,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
       float M = kNoLogit, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < kQ4Cluster; ++v) M = fmaxf(M, ml[v].x);
+      for (int v = 0; v < kQ4Cluster; ++v)
+        if (v < a.spread) M = fmaxf(M, ml[v].x);
 #pragma unroll
       for (int v = 0; v < kQ4Cluster; ++v) {
         if (ml[v].y == 0.f) continue;
@@ -896,10 +898,10 @@ static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int items = a.B * a.Hk * a.row_blocks;
-  const int grid = a.spread ? items * kQ4Cluster : std::min(a.most_tiles, C::CTAS * 152);
+  const int grid = a.spread ? items * a.spread : std::min(a.most_tiles, C::CTAS * 152);
   mark(marks, true, 0, stream);
   e = launch_cluster_maybe_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, marks == nullptr,
-                               a.spread ? kQ4Cluster : 1, a);
+                               std::max(a.spread, 1), a);
   mark(marks, false, 0, stream);
   if (e != cudaSuccess || a.spread) return e;
   mark(marks, true, 1, stream);
