@@ -709,43 +709,55 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, dq_out,
 # ---------------------------------------------------------------------------
 def _check_append(where, q, k, v, cos, sin, positions, slots, q_out):
     """Checks what both forms of the append take besides the cache: (device,
-    the C call's sizes up to max_pos, its token strides)."""
+    the C call's pointers up to q_out, its sizes up to max_pos, its strides)."""
     torch = _torch or _load_torch()
     dev = _cuda_index(where, k)
-    ks = k.shape
+    ks, bf16, i32 = k.shape, torch.bfloat16, torch.int32
     if len(ks) != 3:
         raise ValueError(f"{where}: k and v are [T, H_kv, d], q [T, H, d]; got {tuple(ks)}")
     T, H_kv, d = ks
-    sk, sv = _heads_stride(where, "k", k, T, H_kv, d, dev), _heads_stride(where, "v", v, T, H_kv, d, dev)
-    H, sq = 0, 0
-    i32 = torch.int32
-    if (q is None) != (q_out is None):
-        raise ValueError(f"{where}: q and q_out go together")
-    if q is not None:
-        if len(q.shape) != 3:
-            raise ValueError(f"{where}: q is [T, H, d]; got {tuple(q.shape)}")
-        H = q.shape[1]
+    kst, vst = k.stride(), v.stride()
+    if (k.dtype is not bf16 or v.dtype is not bf16 or v.shape != ks or v.get_device() != dev
+            or kst[1:] != (d, 1) or vst[1:] != (d, 1)):
+        _heads_stride(where, "k", k, T, H_kv, d, dev)
+        _heads_stride(where, "v", v, T, H_kv, d, dev)
+    sk, sv = (kst[0], vst[0]) if T > 1 else (H_kv * d, H_kv * d)
+    H = sq = qp = qo = None
+    if q is not None and q_out is not None:
+        qs = q.shape
+        if len(qs) != 3:
+            raise ValueError(f"{where}: q is [T, H, d]; got {tuple(qs)}")
+        H = qs[1]
         sq = _heads_stride(where, "q", q, T, H, d, dev)
-        if q_out.dtype is not torch.bfloat16 or q_out.shape != (T, H, d) or not q_out.is_contiguous() \
-                or q_out.get_device() != dev:
-            _refuse(where, dev, (("q_out", q_out, torch.bfloat16, (T, H, d)),))
+        if q_out.dtype is not bf16 or q_out.shape != qs or not q_out.is_contiguous() or q_out.get_device() != dev:
+            _refuse(where, dev, (("q_out", q_out, bf16, qs),))
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
+        raise ValueError(f"{where}: q and q_out go together")
     if slots.dtype is not i32 or slots.shape != (T,) or not slots.is_contiguous() or slots.get_device() != dev:
         _refuse(where, dev, (("slots", slots, i32, (T,)),))
-    if cos is None and sin is None:
-        return dev, (T, H, H_kv, d, 0, 1), (sq, sk, sv)
-    if cos is None or sin is None or len(cos.shape) != 2:
-        raise ValueError(f"{where}: cos and sin are both [max_pos, rot / 2], or both None")
-    f32, table = torch.float32, cos.shape
-    if (cos.dtype is not f32 or not cos.is_contiguous() or cos.get_device() != dev
-            or sin.dtype is not f32 or sin.shape != table or not sin.is_contiguous() or sin.get_device() != dev):
-        _refuse(where, dev, (("cos", cos, f32, table), ("sin", sin, f32, table)))
-    if positions is None:
-        if table[1]:
-            raise ValueError(f"{where}: a rotation needs positions")
-    elif positions.dtype is not i32 or positions.shape != (T,) or not positions.is_contiguous() \
-            or positions.get_device() != dev:
-        _refuse(where, dev, (("positions", positions, i32, (T,)),))
-    return dev, (T, H, H_kv, d, 2 * table[1], table[0]), (sq, sk, sv)
+    cp = sp = pp = None
+    rot, max_pos = 0, 1
+    if cos is not None and sin is not None:
+        f32, table = torch.float32, cos.shape
+        if len(table) != 2:
+            raise ValueError(f"{where}: cos and sin are [max_pos, rot / 2]; got {tuple(table)}")
+        if (cos.dtype is not f32 or not cos.is_contiguous() or cos.get_device() != dev
+                or sin.dtype is not f32 or sin.shape != table or not sin.is_contiguous() or sin.get_device() != dev):
+            _refuse(where, dev, (("cos", cos, f32, table), ("sin", sin, f32, table)))
+        max_pos, rot = table[0], 2 * table[1]
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    elif cos is not None or sin is not None:
+        raise ValueError(f"{where}: cos and sin go together")
+    if positions is not None:
+        if positions.dtype is not i32 or positions.shape != (T,) or not positions.is_contiguous() \
+                or positions.get_device() != dev:
+            _refuse(where, dev, (("positions", positions, i32, (T,)),))
+        pp = positions.data_ptr()
+    elif rot:
+        raise ValueError(f"{where}: a rotation needs positions")
+    return (dev, (qp, k.data_ptr(), v.data_ptr(), cp, sp, pp, slots.data_ptr(), qo),
+            (T, H or 0, H_kv, d, rot, max_pos), (sq or 0, sk, sv))
 
 
 def fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, interleaved: bool = False,
@@ -755,7 +767,7 @@ def fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, i
     projection); the rotated width is 2 * cos.shape[1]. q and q_out may both
     be None, and so may cos, sin and positions (no rotation)."""
     where = "fa_kv_append"
-    dev, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
+    dev, ptrs, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
     cs, bf16 = k_cache.shape, _torch.bfloat16
     if len(cs) != 4 or cs[2:] != k.shape[1:]:
         raise ValueError(f"{where}: the caches are [num_blocks, block_size, H_kv, d]; got {tuple(cs)}")
@@ -763,9 +775,9 @@ def fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, i
             or v_cache.dtype is not bf16 or v_cache.shape != cs or not v_cache.is_contiguous()
             or v_cache.get_device() != dev):
         _refuse(where, dev, (("k_cache", k_cache, bf16, cs), ("v_cache", v_cache, bf16, cs)))
-    st = _on_device(dev, (_LIB or load_library()).fa_kv_append, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(cos),
-                    _ptr(sin), _ptr(positions), slots.data_ptr(), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-                    *sizes, cs[0], cs[1], *strides, int(bool(interleaved)), _raw_stream(where, dev, stream))
+    args = (*ptrs, k_cache.data_ptr(), v_cache.data_ptr(), *sizes, cs[0], cs[1], *strides, 1 if interleaved else 0,
+            _raw_stream(where, dev, stream))
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_append, *args)
     if st != FA_OK:
         raise FaError(st, where)
 
@@ -809,12 +821,11 @@ def fa_kv_append_q4(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scale
                     interleaved: bool = False, stream=None) -> None:
     """fa_kv_append for a cache held in 4 bits; same semantics as the C entry point."""
     where = "fa_kv_append_q4"
-    dev, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
+    dev, ptrs, sizes, strides = _check_append(where, q, k, v, cos, sin, positions, slots, q_out)
     num_blocks, _, block_size, _ = _check_q4(where, dev, k_codes, k_scales, v_codes, v_scales, sizes[2], sizes[3])
-    st = _on_device(dev, (_LIB or load_library()).fa_kv_append_q4, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(cos),
-                    _ptr(sin), _ptr(positions), slots.data_ptr(), _ptr(q_out), k_codes.data_ptr(),
-                    k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *sizes, num_blocks, block_size,
-                    *strides, int(bool(interleaved)), _raw_stream(where, dev, stream))
+    args = (*ptrs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *sizes,
+            num_blocks, block_size, *strides, 1 if interleaved else 0, _raw_stream(where, dev, stream))
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_append_q4, *args)
     if st != FA_OK:
         raise FaError(st, where)
 
@@ -852,10 +863,10 @@ def fa_kv_gather_q4(k_codes, k_scales, v_codes, v_scales, block_table, starts, c
     if starts is not None and (starts.dtype is not i32 or starts.shape != (batch,) or not starts.is_contiguous()
                                or starts.get_device() != dev):
         _refuse(where, dev, (("starts", starts, i32, (batch,)),))
-    st = _on_device(dev, (_LIB or load_library()).fa_kv_gather_q4, k_codes.data_ptr(), k_scales.data_ptr(),
-                    v_codes.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), _ptr(starts),
-                    cu_seqlens_k.data_ptr(), k.data_ptr(), v.data_ptr(), batch, H_kv, d, ks[0], num_blocks, block_size,
-                    width, _raw_stream(where, dev, stream))
+    args = (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(),
+            _ptr(starts), cu_seqlens_k.data_ptr(), k.data_ptr(), v.data_ptr(), batch, H_kv, d, ks[0], num_blocks,
+            block_size, width, _raw_stream(where, dev, stream))
+    st = _on_device(dev, (_LIB or load_library()).fa_kv_gather_q4, *args)
     if st != FA_OK:
         raise FaError(st, where)
 
@@ -901,11 +912,11 @@ def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_ta
     n_new, max_seq_len = qs[1] if len(qs) == 4 else 1, int(max_seq_len)
     workspace = _workspace(where, workspace, dev, stream, fa_decode_paged_q4_workspace_size, B, n_new, H, H_kv, d,
                            max_seq_len)
-    st = _on_device(dev, (_LIB or load_library()).fa_decode_paged_q4, q.data_ptr(), k_codes.data_ptr(),
-                    k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                    block_table.data_ptr(), seq_lens.data_ptr(), B, n_new, H, H_kv, d, num_blocks, block_size, width,
-                    max_seq_len, float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                    _raw_stream(where, dev, stream))
+    args = (q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+            o.data_ptr(), lse.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), B, n_new, H, H_kv, d,
+            num_blocks, block_size, width, max_seq_len, float(scale), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _raw_stream(where, dev, stream))
+    st = _on_device(dev, (_LIB or load_library()).fa_decode_paged_q4, *args)
     if st != FA_OK:
         raise FaError(st, where)
 
