@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-constexpr float kNoLogit = -1e30f;  // the maximum before the first key; below every finite logit
+constexpr float kNoLogit = -3.402823466e38f;  // the maximum before the first key; no finite logit is below it
 
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   return min(max(a.seq_lens[b], 0), a.max_seq_len);
