@@ -157,12 +157,20 @@ __device__ __forceinline__ long long q4_row(const Q4DecodeArgs& a, int b, int kv
   return (static_cast<long long>(b) * a.n_new + row / G) * a.H + kvh * G + row % G;
 }
 
+// The first of the two columns (rows of the queries) whose logits lane (., c)
+// works on. With up to four rows the columns from 4 on are empty, and the lanes
+// that have them take the first ones' logits of the stage's other 16 keys.
+template <bool FEW>
+__device__ __forceinline__ int column(int c) {
+  return FEW ? 2 * (c & 1) : 2 * c;
+}
+
 // What a lane holds of the queries: lane (r, c) = (lane / 4, lane % 4).
 template <int D, int NT>
 struct Q4Rows {
   static constexpr int NG = D / 64;
   uint32_t q[NT][NG][4][2];  // B fragments of row 8 j + r, k-step t of group g
-  float qs[NT][2];           // of rows 8 j + 2 c + {0, 1}: what a product of codes is multiplied by
+  float qs[NT][2];           // of rows 8 j + column + {0, 1}: what a product of codes is multiplied by
   float sum[NT][NG][2];      // scale log2e times the sum of the row's group
 };
 
@@ -186,7 +194,7 @@ struct Q4Raw {
   }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool FEW>
 __device__ __forceinline__ void q4_rows(const Q4DecodeArgs& a, const Q4Raw<D, NT>& raw, int lane, Q4Rows<D, NT>& R) {
   constexpr int NG = D / 64;
   const int c = lane & 3;
@@ -229,17 +237,18 @@ __device__ __forceinline__ void q4_rows(const Q4DecodeArgs& a, const Q4Raw<D, NT
       }
     }
     const float down = a.scale_log2 * pow2(24 - shift);
-    // To the lanes of the C fragments' columns: row 8 j + 2 c + i comes from lane (2 c + i, .).
+    // To the lanes of the C fragments' columns: row 8 j + x comes from lane (x, .).
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      R.qs[j][i] = __shfl_sync(0xffffffffu, down, (2 * c + i) * 4);
+      const int x = column<FEW>(c) + i;
+      R.qs[j][i] = __shfl_sync(0xffffffffu, down, x * 4);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) R.sum[j][g][i] = __shfl_sync(0xffffffffu, s[g], (2 * c + i) * 4);
+      for (int g = 0; g < NG; ++g) R.sum[j][g][i] = __shfl_sync(0xffffffffu, s[g], x * 4);
     }
   }
 }
 
-// Running softmax of a lane's columns (rows 8 j + 2 c + {0, 1}): maximum and
+// Running softmax of a lane's columns (rows 8 j + column + {0, 1}): maximum and
 // powers are the same in all lanes of a column, the sums are the lane's own.
 template <int D, int NT>
 struct Q4State {
@@ -266,25 +275,26 @@ struct Q4State {
 };
 
 // The largest of a column over its lanes.
+template <bool FEW>
 __device__ __forceinline__ float column_max(float x) {
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  for (int off = FEW ? 2 : 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
   return x;
 }
 
 // The keys of a stage. MASKED: some of them may be hidden from some rows (row x
 // sees the keys below open + (row0 + x) / G - row0 / G) or past the sequence
 // (`left` of them are in it).
-template <int D, int NT, bool MASKED>
+template <int D, int NT, bool FEW, bool MASKED>
 __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, int open, int row0, int G,
                                         const Q4Rows<D, NT>& R, Q4State<D, NT>& S) {
   using C = Q4Cfg<D, NT>;
-  constexpr int NG = D / 64, KH = 2 * C::HALVES;  // key ka + 8 h of a lane, h < KH
+  constexpr int NG = D / 64, KH = FEW ? 2 : 2 * C::HALVES;  // logits of keys kl + 8 h of a lane, h < KH
   const int r = lane >> 2, c = lane & 3;
   // Row i of the A operand of Q K^T, and k index i of P V, is key (i >> 1) + 4 (i & 1)
   // of its eight: the lanes of a load then meet two banks' worth of rows, not one.
-  const int ka = (r >> 1) + 4 * (r & 1);
-  float sc[NT][KH][2];  // [key ka + 8 h][row i]
+  const int ka = (r >> 1) + 4 * (r & 1), kl = FEW ? ka + 8 * (c & 2) : ka;
+  float sc[NT][KH][2];  // [key kl + 8 h][row i]
   uint32_t vsz[NG][KH];
   float acc[C::HALVES][NT][NG][4];
   {
@@ -316,37 +326,43 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
       }
     }
   }
+  if constexpr (FEW) {
 #pragma unroll
-  for (int s = 0; s < C::HALVES; ++s) {
+    for (int g = 0; g < NG; ++g) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int h = 2 * s + e;
-      const uint32_t* pk = reinterpret_cast<const uint32_t*>(st + C::OFF_KS) + (ka + 8 * h) * NG;
-      const uint32_t* pv = reinterpret_cast<const uint32_t*>(st + C::OFF_VS) + (ka + 8 * h) * NG;
-      const bool on = !MASKED || ka + 8 * h < left;
-      uint32_t ksz[NG];
-      if constexpr (NG == 2) {
-        const uint2 k = *reinterpret_cast<const uint2*>(pk), v = *reinterpret_cast<const uint2*>(pv);
-        ksz[0] = k.x, ksz[1] = k.y, vsz[0][h] = v.x, vsz[1][h] = v.y;
-      } else {
-        ksz[0] = *pk, vsz[0][h] = *pv;
+      for (int i = 0; i < 4; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, acc[1][0][g][i], 2);
+        acc[0][0][g][i] = (c & 2) ? other : acc[0][0][g][i];
       }
-      if (!on) {
+    }
+  }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) ksz[g] = vsz[g][h] = 0u;
-      }
+  for (int h = 0; h < KH; ++h) {
+    const int s = h / 2, e = h % 2;
+    const uint32_t* pk = reinterpret_cast<const uint32_t*>(st + C::OFF_KS) + (kl + 8 * h) * NG;
+    const uint32_t* pv = reinterpret_cast<const uint32_t*>(st + C::OFF_VS) + (kl + 8 * h) * NG;
+    uint32_t ksz[NG];
+    if constexpr (NG == 2) {
+      const uint2 k = *reinterpret_cast<const uint2*>(pk), v = *reinterpret_cast<const uint2*>(pv);
+      ksz[0] = k.x, ksz[1] = k.y, vsz[0][h] = v.x, vsz[1][h] = v.y;
+    } else {
+      ksz[0] = *pk, vsz[0][h] = *pv;
+    }
+    if (MASKED && kl + 8 * h >= left) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int g = 0; g < NG; ++g) ksz[g] = vsz[g][h] = 0u;
+    }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = acc[s][j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
-          for (int g = 1; g < NG; ++g) {
-            x = fmaf(acc[s][j][g][2 * e + i], lo_f(ksz[g]), x);
-            y = fmaf(hi_f(ksz[g]), R.sum[j][g][i], y);
-          }
-          sc[j][h][i] = fmaf(x, R.qs[j][i], y);
+      for (int i = 0; i < 2; ++i) {
+        float x = acc[s][j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
+#pragma unroll
+        for (int g = 1; g < NG; ++g) {
+          x = fmaf(acc[s][j][g][2 * e + i], lo_f(ksz[g]), x);
+          y = fmaf(hi_f(ksz[g]), R.sum[j][g][i], y);
         }
+        sc[j][h][i] = fmaf(x, R.qs[j][i], y);
       }
     }
   }
@@ -358,7 +374,7 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         seen[j][h][i] =
-            !MASKED || (ka + 8 * h < left && ka + 8 * h < open + (row0 + j * 8 + 2 * c + i) / G - row0 / G);
+            !MASKED || (kl + 8 * h < left && kl + 8 * h < open + (row0 + j * 8 + column<FEW>(c) + i) / G - row0 / G);
         if (!seen[j][h][i]) sc[j][h][i] = -INFINITY;
       }
     }
@@ -402,7 +418,7 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
         float mn = S.m[j][i];
 #pragma unroll
         for (int h = 0; h < KH; ++h) mn = fmaxf(mn, sc[j][h][i]);
-        mn = column_max(mn);
+        mn = column_max<FEW>(mn);
         const float alpha = ex2(S.m[j][i] - mn);
         S.m[j][i] = mn;
         S.l[j][i] *= alpha;
@@ -413,7 +429,7 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
 #pragma unroll
           for (int h = 0; h < KH; ++h)
             if (seen[j][h][i]) mx = fmaxf(mx, ex2(sc[j][h][i] - mn) * lo_f(vsz[g][h]));
-          mx = column_max(mx);
+          mx = column_max<FEW>(mx);
           if (mx * S.up[j][g][i] >= 0x1p15f) {  // (the same in all lanes of the column)
             const float up = pow2(min(9 - exponent(mx), 120));
             f *= up * inverse_pow2(S.up[j][g][i]);
@@ -445,8 +461,14 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
     for (int g = 0; g < NG; ++g) {
       uint32_t bp[NT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        bp[j][0] = transpose8(ph[j][g][2 * s]), bp[j][1] = transpose8(ph[j][g][2 * s + 1]);
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // (FEW: each half's own P stands in the first four columns, the other's in the empty ones.)
+          const uint32_t x = ph[j][g][FEW ? e : 2 * s + e];
+          bp[j][e] = transpose8(FEW && s == 1 ? __shfl_xor_sync(0xffffffffu, x, 2) : x);
+        }
+      }
       // Word r of the group of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (as k indices).
       uint32_t w[4];
 #pragma unroll
@@ -626,7 +648,7 @@ __device__ __forceinline__ Q4Start q4_start_spread(const Q4DecodeArgs& a) {
   return at;
 }
 
-template <int D, int NT, bool SPREAD>
+template <int D, int NT, bool FEW, bool SPREAD>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_decode_q4_kernel(const Q4DecodeArgs a) {
   using C = Q4Cfg<D, NT>;
   constexpr int NG = C::NG;
@@ -671,7 +693,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
             w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1), at.shares.of(at.run_end - w.left + w.n - 1))
                          : make_int4(-1, 0, 0, 0);
       Q4Rows<D, NT> R;
-      q4_rows<D, NT>(a, raw, lane, R);
+      q4_rows<D, NT, FEW>(a, raw, lane, R);
       Q4State<D, NT> S;
       S.clear();
       // Of the tile's keys of this warp: those in the sequence, and those that every row sees.
@@ -683,12 +705,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
         copies.copy(a, stage == 0 ? C::STAGES - 1 : stage - 1, warp, lane);
         const uint8_t* st = ring + stage * C::STAGE_BYTES;
         stage = stage == C::STAGES - 1 ? 0 : stage + 1;
-        if (open >= C::KEYS) q4_step<D, NT, false>(st, lane, 0, 0, 0, 1, R, S);
-        else if (left > 0) q4_step<D, NT, true>(st, lane, left, open, row0, G, R, S);
+        if (open >= C::KEYS) q4_step<D, NT, FEW, false>(st, lane, 0, 0, 0, 1, R, S);
+        else if (left > 0) q4_step<D, NT, FEW, true>(st, lane, left, open, row0, G, R, S);
         left -= kQ4Tile, open -= kQ4Tile;
       }
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
+      for (int off = FEW ? 2 : 4; off < 32; off <<= 1) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -895,11 +917,11 @@ __global__ void __launch_bounds__(512, 2) fa_decode_q4_join_kernel(const Q4Decod
   if (lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FEW>
 static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* marks) {
   using C = Q4Cfg<D, NT>;
   static_assert(C::CTAS * 152 <= kQ4MaxCtas, "the workspace holds every CTA's parts");
-  auto kern = a.spread ? fa_decode_q4_kernel<D, NT, true> : fa_decode_q4_kernel<D, NT, false>;
+  auto kern = a.spread ? fa_decode_q4_kernel<D, NT, FEW, true> : fa_decode_q4_kernel<D, NT, FEW, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int items = a.B * a.Hk * a.row_blocks;
@@ -921,9 +943,14 @@ static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const
   return e;
 }
 
+template <int D>
+static cudaError_t launch_q4_d(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* m) {
+  if (a.rows_per > 8) return launch_q4_t<D, 2, false>(a, stream, m);
+  return a.n_new * (a.H / a.Hk) > 4 ? launch_q4_t<D, 1, false>(a, stream, m) : launch_q4_t<D, 1, true>(a, stream, m);
+}
+
 cudaError_t launch_decode_q4(const Q4DecodeArgs& a, cudaStream_t stream, const LaunchMarks* m) {
-  if (a.rows_per == 8) return a.D == 64 ? launch_q4_t<64, 1>(a, stream, m) : launch_q4_t<128, 1>(a, stream, m);
-  return a.D == 64 ? launch_q4_t<64, 2>(a, stream, m) : launch_q4_t<128, 2>(a, stream, m);
+  return a.D == 64 ? launch_q4_d<64>(a, stream, m) : launch_q4_d<128>(a, stream, m);
 }
 
 }  // namespace fa
