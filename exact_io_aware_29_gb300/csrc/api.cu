@@ -1341,19 +1341,20 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   // A cluster for each item, as many CTAs as leave room for all clusters at once
   // and have a tile each, unless a CTA would have many tiles to go through, or
   // more than the shares of an even split. (32/8 heads, d 128, in us, split evenly
-  // and in clusters of 8, 4, 2 and 1: one sequence of 1000 tokens 8.0, 7.0, 7.4,
-  // 8.6; 8 of 3000 15.9, 18.6, 12.2, 14.4; 16 of 3000 24.2, 31, 26, 18.5, 21.8; 48
-  // of 1000 23.1, -, -, 24.8, 18.3; 256 of 1000 72.2, -, -, 99, 70.7. One of 30000
-  // 17.9, 25.3; one of 8000 with one key head 8.8, 10.8; 16 of 8000 34.3, 46, 39,
-  // 35.6; 80 of 3000 58.9, -, -, 63, 61.)
+  // and in clusters of 8, 4, 2 and 1: one sequence of 1000 tokens 7.7, 6.6, 7.0,
+  // 8.1, 9.5; 8 of 3000 13.7, 17.8, 11.4, 13.5, 20; 16 of 3000 22.7, 30, 24, 17.4,
+  // 21; 48 of 1000 22, 57, 35, 24, 17.4; 256 of 1000 66, 276, 150, 95, 67. One of
+  // 30000 17.3, 25; 16 of 8000 32.3, 44, 38, 33.5; 80 of 3000 54, 116, 75, 60, 58;
+  // with one key head, 1, 4 and 16 of 8000 8.7, 10.0 and 15.7, in clusters of 8
+  // 10.7, 11.1 and 13.7.)
   int cs = fa::kQ4Cluster;
   while (cs > 1 && (items * cs > ctas || cs / 2 >= tiles)) cs /= 2;
   const int most = cs == 1 ? 8 : (items * cs * 2 > ctas ? 16 : (items >= 8 ? 8 : 6));
   a->spread = (tiles + cs - 1) / cs <= most ? cs : 0;
   // Few items can have many parts each: then eight warps join a row, a CTA two
   // rows of an item. (One sequence of 131072 tokens, 8 key heads, 57 parts each:
-  // 33.7 us, 38.1 with the joins by CTA; four of up to 1200, 4 key heads, 10
-  // parts: 9.7 and 9.0.)
+  // 32.8 us, 37.3 with the joins by CTA; four of up to 1200, 4 key heads, 10 parts:
+  // 9.2 and 8.8.)
   a->cuts_by_item = std::min<long long>(a->most_tiles, ctas) / items >= 32;
   return FA_OK;
 }

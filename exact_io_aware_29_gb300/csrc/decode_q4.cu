@@ -23,8 +23,8 @@
 //   O to bf16 costs), at terms down to 2^-23 of the largest. (As the sum of two
 //   bf16 numbers, whose exponents need no care, it takes twice the products and
 //   a third more instructions.)
-// The logic pipe, not the tensor cores, stands nearest to HBM: about 130
-// instructions on it for 16 keys, of 200 that HBM leaves time for (d 128).
+// The logic pipe, not the tensor cores, stands nearest to HBM: about 125
+// instructions on it for 16 keys, of 205 that HBM leaves time for (d 128).
 //
 // A persistent grid shares the 128-key tiles of all sequences and key heads out
 // evenly, in order, whatever their lengths: a CTA takes a run of tiles, whole
@@ -38,9 +38,9 @@
 // A step of few, short sequences goes another way, its time being a sum of
 // latencies: a cluster of up to eight CTAs shares an item's tiles and joins its
 // parts through their shared memory.
-// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 66 us, 5.0 TB/s (the
-// copies alone 60, the arithmetic alone 61); one of 131072: 34 us, 4.4 TB/s, of
-// which about 8 are spent before the first tile and after the last.
+// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 60.6 us, 5.4 TB/s (the
+// copies alone 59); one of 131072: 32.9 us, 4.6 TB/s. About 8 of them are spent
+// before the first tile and after the last.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -527,7 +527,7 @@ struct Q4Copies {
       const int block = key / a.block_size;
       const int phys = a.block_table[static_cast<long long>(w.b) * a.max_blocks + block];
       if (phys >= 0 && phys < a.num_blocks)
-        row = (static_cast<long long>(phys) * a.Hk + w.item / a.row_blocks) * a.block_size + (key - block * a.block_size);
+        row = (static_cast<long long>(phys) * a.Hk + w.item / a.row_blocks) * a.block_size + key - block * a.block_size;
     }
   }
   // The next tile's keys into stage s (an empty group past the end).
@@ -574,7 +574,7 @@ template <int D, int NT>
 __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem, int warp, int lane) {
   using C = Q4Cfg<D, NT>;
   long long* warp_sum = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
-  int* found = reinterpret_cast<int*>(warp_sum + C::WARPS);  // sequence of the CTA's first tile, units of those before it
+  int* found = reinterpret_cast<int*>(warp_sum + C::WARPS);  // sequence of the first tile, units of those before it
   // The tiles of all sequences (and, in the upper half, how many have any), and
   // the sequence that this CTA's run starts in: each thread adds up a stretch of
   // sequences, then their sums are scanned.
@@ -602,7 +602,7 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
   }
   // An item costs about three tiles' time besides its tiles (its queries, the
   // first steps' maxima, the join of the warps): 64 sequences of up to 8192
-  // tokens 65.5 us, 71.7 if it is left out. Where runs are short, what counts is
+  // tokens 60.6 us, 71.0 if it is left out. Where runs are short, what counts is
   // the longest of them: only tiles then.
   const int tiles = static_cast<int>(all) * items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
       raw.read(a, w.b, kvh, row0, rows, lane);
       if (!SPREAD && threadIdx.x == 0 && w.tile == 0 && (a.cuts_by_item || w.here < w.n))
         a.cuts[a.cuts_by_item ? w.b * items + w.item : cta] =
-            w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1), at.shares.of(at.run_end - w.left + w.n - 1))
+            w.here < w.n ? make_int4(w.b, w.item, 2 * cta + (first_item ? 0 : 1),
+                                     at.shares.of(at.run_end - w.left + w.n - 1))
                          : make_int4(-1, 0, 0, 0);
       Q4Rows<D, NT> R;
       q4_rows<D, NT, FEW>(a, raw, lane, R);
@@ -937,7 +938,8 @@ static cudaError_t launch_q4_t(const Q4DecodeArgs& a, cudaStream_t stream, const
     e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 8>, dim3(items, (rows + 1) / 2), dim3(512), 0, stream,
                          marks == nullptr, a);
   } else {
-    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 1>, dim3(grid), dim3(32 * C::ROWS), 0, stream, marks == nullptr, a);
+    e = launch_maybe_pdl(fa_decode_q4_join_kernel<D, 1>, dim3(grid), dim3(32 * C::ROWS), 0, stream, marks == nullptr,
+                         a);
   }
   mark(marks, false, 1, stream);
   return e;

@@ -124,7 +124,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[4], uint32_t& s
   inv *= 1.f - 0x1p-21f;  // 2^-23 off at most: now between (1 - 2^-20) / s and 1 / s
   const int half = __float_as_int(0.5f * s);
   const float magic = 12582912.f;  // 1.5 2^23: sums with it are integers, in their low bits
-  const uint64_t lo2f = f2_pack(lo, lo), inv2 = f2_pack(inv, inv), magic2 = f2_pack(magic, magic), minus = f2_pack(-s, -s);
+  const uint64_t lo2f = f2_pack(lo, lo), inv2 = f2_pack(inv, inv), magic2 = f2_pack(magic, magic);
+  const uint64_t minus = f2_pack(-s, -s);
   uint32_t codes = 0u - 0x4B400000u * 0x11111111u;  // the bits of 1.5 2^23 in each term, taken out
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -195,9 +196,10 @@ __global__ void __launch_bounds__(256, R == 8 ? 4 : 5) fa_kv_append_kernel(const
   if (section < 2) turn.load(a, token, l * 8, lane, live);
   const int block = slot / a.block_size;
   // First head's row of the output, in rows of d elements.
-  const long long row = section == 0 ? token * a.H + head0
-                        : Q4 ? (static_cast<long long>(block) * a.Hk + head0) * a.block_size + (slot - block * a.block_size)
-                             : static_cast<long long>(slot) * a.Hk + head0;
+  const long long row =
+      section == 0 ? token * a.H + head0
+      : Q4         ? (static_cast<long long>(block) * a.Hk + head0) * a.block_size + slot - block * a.block_size
+                   : static_cast<long long>(slot) * a.Hk + head0;
   void* out = section == 0 ? a.q_out : (section == 1 ? a.k_cache : a.v_cache);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(256, R == 8 ? 4 : 5) fa_kv_append_kernel(const
     if (section < 2) turn.apply(w);
     if (!Q4 || section == 0) {
       if (i < n)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (row + i) * D + l * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (row + i) * D + l * 8) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t sz;
       const uint32_t codes = quantise(w, sz);
@@ -328,7 +331,8 @@ static cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
-  if (a.k_scales != nullptr) return a.D == 64 ? launch_append_t<64, true>(a, stream) : launch_append_t<128, true>(a, stream);
+  if (a.k_scales != nullptr)
+    return a.D == 64 ? launch_append_t<64, true>(a, stream) : launch_append_t<128, true>(a, stream);
   return a.D == 64 ? launch_append_t<64, false>(a, stream) : launch_append_t<128, false>(a, stream);
 }
 
