@@ -16,7 +16,7 @@
 // low bits of an f16 is code 2^-24 (a subnormal, exact), four bits further up
 // code 2^-20, so one AND makes two codes.
 //   Q K^T: the row of q is scaled to [2^14, 2^15) by a power of two, so that its
-//   f16 is exact (below 2^-29 of the row's largest: rounded at 2^-40 of it).
+//   f16 is exact (below 2^-27 of the row's largest: rounded at 2^-35 of it).
 //   P V: p s is scaled by a power of two of the row and group, such that the
 //   largest so far is at most 2^15 and was 2^9 or more when the power was
 //   chosen: rounded to f16, 2^-11 of a term (an eighth of what the rounding of

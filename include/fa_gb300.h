@@ -457,8 +457,9 @@ int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_cod
  *   workspace      >= fa_decode_paged_q4_workspace_size(...) bytes, 16-byte
  *                  aligned, caller-owned. Calls that overlap on the GPU need
  *                  workspaces of their own.
- * Logits, softmax and sums are those of the cache's values z + s * code as they
- * are, in fp32 (a row of q with elements of 2^114 or more may give NaN).
+ * The values are z + s * code as they are, not rounded; logits, softmax and sums
+ * are fp32, and p * s enters its product as f16 (after a power of two: 2^-11 of
+ * each term). A row of q with elements of 2^114 or more may give NaN.
  * Results are bitwise repeatable. Lengths and tables are checked on the host
  * only in check mode (FA_CHECK=1); otherwise lengths are clamped to
  * [0, max_seq_len] and block ids outside [0, num_blocks) read as zero keys and
