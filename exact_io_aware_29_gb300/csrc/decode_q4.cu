@@ -114,11 +114,11 @@ __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int q4_tiles(int L) { return (L + kQ4Tile - 1) / kQ4Tile; }
 // How `total` units of work are shared out over `ctas` CTAs: runs of `per` or
-// per + 1, the longer ones first. A unit is a tile; an item counts as `head`
-// units more, in front of its tiles.
+// per + 1, the longer ones first. A unit is a tile; an item may count as some
+// units more (its head), in front of its tiles.
 struct Q4Shares {
-  int per, longer, head;
-  __device__ __forceinline__ Q4Shares(int total, int ctas, int h) : per(total / ctas), longer(total % ctas), head(h) {}
+  int per, longer;
+  __device__ __forceinline__ Q4Shares(int total, int ctas) : per(total / ctas), longer(total % ctas) {}
   __device__ __forceinline__ int start(int c) const { return c * per + min(c, longer); }
   __device__ __forceinline__ int of(int unit) const {  // the CTA that has it
     const int x = longer * (per + 1);
@@ -607,7 +607,7 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
   const int tiles = static_cast<int>(all) * items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
   const int head = tiles >= 8 * ctas ? kQ4Head : 0;
-  const Q4Shares shares(tiles + head * static_cast<int>(all >> 32) * items, max(ctas, 1), head);
+  const Q4Shares shares(tiles + head * static_cast<int>(all >> 32) * items, max(ctas, 1));
   auto units = [&](long long sum) { return (static_cast<int>(sum) + head * static_cast<int>(sum >> 32)) * items; };
   const int start = shares.start(cta);
   if (cta < ctas && start >= units(before) && start < units(before + own)) {
@@ -636,7 +636,7 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
 // The same for an item shared by a cluster: its tiles in equal runs.
 template <int D, int NT>
 __device__ __forceinline__ Q4Start q4_start_spread(const Q4DecodeArgs& a) {
-  Q4Start at{Q4Walk{}, 0, 0, Q4Shares(0, 1, 0)};
+  Q4Start at{Q4Walk{}, 0, 0, Q4Shares(0, 1)};
   const int items = a.Hk * a.row_blocks, id = blockIdx.x / a.spread, rank = blockIdx.x - id * a.spread;
   Q4Walk& w = at.w;
   w.b = id / items;
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::CTAS) fa_
     if (q4_len(a, b) > 0) continue;
     const long long row = static_cast<long long>(b) * a.n_new * a.H;
     const int n = a.n_new * a.H;
-    for (int x = threadIdx.x; x < n * (D / 8); x += C::THREADS)
+    for (long long x = threadIdx.x; x < static_cast<long long>(n) * (D / 8); x += C::THREADS)
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + row * D)[x] = make_uint4(0u, 0u, 0u, 0u);
     for (int x = threadIdx.x; x < n; x += C::THREADS) a.lse[row + x] = -INFINITY;
     for (int x = threadIdx.x; a.cuts_by_item && x < items; x += C::THREADS)

@@ -411,7 +411,8 @@ int fa_kv_append(const void* q, const void* k, const void* v, const float* cos, 
  * is past fp32, reads as NaN (s = z = NaN, codes 0).
  *   k_codes, v_codes    device uint8 [num_blocks, H_kv, block_size, d / 2]: byte
  *                       j holds element 2 j in its low half, 2 j + 1 in its high.
- *   k_scales, v_scales  device bf16 [num_blocks, H_kv, block_size, d / 64, 2]: (s, z).
+ *   k_scales, v_scales  device bf16 [num_blocks, H_kv, block_size, d / 64, 2]: (s, z),
+ *                       s >= 0 (a cache written by other means keeps to it).
  *   block_size          a multiple of 16 (FA_ERR_UNSUPPORTED otherwise).
  */
 int fa_kv_append_q4(const void* q, const void* k, const void* v, const float* cos, const float* sin,
