@@ -1333,7 +1333,7 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   a->rows_per = rows <= 8 ? 8 : 16;
   const long long blocks = (rows + a->rows_per - 1) / a->rows_per;
   const long long tiles = (static_cast<long long>(max_seq_len) + fa::kQ4Tile - 1) / fa::kQ4Tile;
-  if (rows * B * H_kv > 0x7fffffffLL || (tiles + fa::kQ4Head) * B * H_kv > 0x7fffffffLL / blocks)
+  if (rows * B * H_kv > 0x7fffffffLL || (tiles + fa::q4_head(a->rows_per)) * B * H_kv > 0x7fffffffLL / blocks)
     return FA_ERR_UNSUPPORTED;
   a->row_blocks = static_cast<int>(blocks);
   a->most_tiles = static_cast<int>(tiles * B * H_kv * blocks);

@@ -300,7 +300,7 @@ struct Q4DecodeArgs {
   int4* cuts;                 // [kQ4MaxCtas]: (sequence or -1, item of it, first part, last CTA)
 };
 constexpr int kQ4Tile = 128;           // keys of a tile
-constexpr int kQ4Head = 3;             // an item's cost besides its tiles, in tiles
+constexpr int q4_head(int rows_per) { return rows_per > 8 ? 6 : 3; }  // an item's cost besides its tiles, in tiles
 constexpr int kQ4Cluster = 8;          // most CTAs of a cluster
 constexpr int q4_ctas(int D, int rows_per) { return (D == 64 ? 4 : 3) - (rows_per > 8 ? 1 : 0); }  // CTAs per SM
 constexpr int kQ4MaxCtas = 4 * 152;

@@ -38,8 +38,8 @@
 // A step of few, short sequences goes another way, its time being a sum of
 // latencies: a cluster of up to eight CTAs shares an item's tiles and joins its
 // parts through their shared memory.
-// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 60.6 us, 5.4 TB/s (the
-// copies alone 59); one of 131072: 32.9 us, 4.6 TB/s. About 8 of them are spent
+// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 60.0 us, 5.5 TB/s (the
+// copies alone 59); one of 131072: 32.7 us, 4.6 TB/s. About 8 of them are spent
 // before the first tile and after the last.
 #include <cuda_bf16.h>
 
@@ -89,6 +89,9 @@ __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
+// Two fp32 numbers for the instructions that work on pairs of them.
+__device__ __forceinline__ uint64_t pair(const float (&x)[2]) { return f2_pack(x[0], x[1]); }
+__device__ __forceinline__ uint64_t both(float x) { return f2_pack(x, x); }
 // max(a, b), NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -354,16 +357,14 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
+      uint64_t x = f2_mul(f2_pack(acc[s][j][0][2 * e], acc[s][j][0][2 * e + 1]), both(lo_f(ksz[0])));
+      uint64_t y = f2_mul(both(hi_f(ksz[0])), pair(R.sum[j][0]));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = acc[s][j][0][2 * e + i] * lo_f(ksz[0]), y = hi_f(ksz[0]) * R.sum[j][0][i];
-#pragma unroll
-        for (int g = 1; g < NG; ++g) {
-          x = fmaf(acc[s][j][g][2 * e + i], lo_f(ksz[g]), x);
-          y = fmaf(hi_f(ksz[g]), R.sum[j][g][i], y);
-        }
-        sc[j][h][i] = fmaf(x, R.qs[j][i], y);
+      for (int g = 1; g < NG; ++g) {
+        x = f2_fma(f2_pack(acc[s][j][g][2 * e], acc[s][j][g][2 * e + 1]), both(lo_f(ksz[g])), x);
+        y = f2_fma(both(hi_f(ksz[g])), pair(R.sum[j][g]), y);
       }
+      f2_unpack(f2_fma(x, pair(R.qs[j]), y), sc[j][h][0], sc[j][h][1]);
     }
   }
   bool seen[NT][KH][2];
@@ -389,12 +390,15 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int h = 0; h < KH; ++h) {
-        const float p0 = ex2(sc[j][h][0] - S.m[j][0]), p1 = ex2(sc[j][h][1] - S.m[j][1]);
-        p[j][h][0] = p0, p[j][h][1] = p1;
+        float x0, x1;
+        f2_unpack(f2_sub(pair(sc[j][h]), pair(S.m[j])), x0, x1);
+        p[j][h][0] = ex2(x0), p[j][h][1] = ex2(x1);
 #pragma unroll
-        for (int g = 0; g < NG; ++g)  // (a hidden key's scale may be NaN)
-          ph[j][g][h] = pack_f16x2((seen[j][h][0] ? p0 * lo_f(vsz[g][h]) : 0.f) * S.up[j][g][0],
-                                   (seen[j][h][1] ? p1 * lo_f(vsz[g][h]) : 0.f) * S.up[j][g][1]);
+        for (int g = 0; g < NG; ++g) {  // (a hidden key's scale may be NaN)
+          f2_unpack(f2_mul(pair(p[j][h]), both(lo_f(vsz[g][h]))), x0, x1);
+          f2_unpack(f2_mul(f2_pack(seen[j][h][0] ? x0 : 0.f, seen[j][h][1] ? x1 : 0.f), pair(S.up[j][g])), x0, x1);
+          ph[j][g][h] = pack_f16x2(x0, x1);
+        }
       }
     }
   };
@@ -445,13 +449,13 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int h = 0; h < KH; ++h) {
+      f2_unpack(f2_add(pair(S.l[j]), pair(p[j][h])), S.l[j][0], S.l[j][1]);
 #pragma unroll
-      for (int h = 0; h < KH; ++h) {
-        S.l[j][i] += p[j][h][i];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          S.z[j][g][i] = fmaf(p[j][h][i], seen[j][h][i] ? hi_f(vsz[g][h]) : 0.f, S.z[j][g][i]);
+      for (int g = 0; g < NG; ++g) {
+        const float z = hi_f(vsz[g][h]);
+        f2_unpack(f2_fma(pair(p[j][h]), f2_pack(seen[j][h][0] ? z : 0.f, seen[j][h][1] ? z : 0.f), pair(S.z[j][g])),
+                  S.z[j][g][0], S.z[j][g][1]);
       }
     }
   }
@@ -601,12 +605,13 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
     all += warp_sum[v];
   }
   // An item costs about three tiles' time besides its tiles (its queries, the
-  // first steps' maxima, the join of the warps): 64 sequences of up to 8192
-  // tokens 60.6 us, 71.0 if it is left out. Where runs are short, what counts is
-  // the longest of them: only tiles then.
+  // first steps' maxima, the join of the warps), six with 9 to 16 rows: 64
+  // sequences of up to 8192 tokens 60.0 us, 70 if it is left out, and 101 with
+  // four drafts each, 111 if it counts as three. Where runs are short, what counts
+  // is the longest of them: only tiles then.
   const int tiles = static_cast<int>(all) * items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
-  const int head = tiles >= 8 * ctas ? kQ4Head : 0;
+  const int head = tiles >= 8 * ctas ? q4_head(C::ROWS) : 0;
   const Q4Shares shares(tiles + head * static_cast<int>(all >> 32) * items, max(ctas, 1));
   auto units = [&](long long sum) { return (static_cast<int>(sum) + head * static_cast<int>(sum >> 32)) * items; };
   const int start = shares.start(cta);
