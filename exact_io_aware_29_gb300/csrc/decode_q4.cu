@@ -18,11 +18,11 @@
 //   Q K^T: the row of q is scaled to [2^14, 2^15) by a power of two, so that its
 //   f16 is exact (below 2^-27 of the row's largest: rounded at 2^-35 of it).
 //   P V: p s is scaled by a power of two of the row and group, such that the
-//   largest so far is at most 2^15 and was 2^9 or more when the power was
-//   chosen: rounded to f16, 2^-11 of a term (an eighth of what the rounding of
-//   O to bf16 costs), at terms down to 2^-23 of the largest. (As the sum of two
-//   bf16 numbers, whose exponents need no care, it takes twice the products and
-//   a third more instructions.)
+//   largest so far, each at its present weight, lies in [2^9, 2^15): rounded to
+//   f16, 2^-11 of a term (an eighth of what the rounding of O to bf16 costs), at
+//   terms down to 2^-23 of the largest (and 2^-134). (As the sum of two bf16
+//   numbers, whose exponents need no care, it takes twice the products and a
+//   third more instructions.)
 // The logic pipe, not the tensor cores, stands nearest to HBM: about 125
 // instructions on it for 16 keys, of 205 that HBM leaves time for (d 128).
 //
@@ -87,6 +87,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+__device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : pow2(e); }
 __device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 // Two fp32 numbers for the instructions that work on pairs of them.
@@ -258,7 +259,7 @@ struct Q4State {
   static constexpr int NG = D / 64;
   float o[NT][NG][4][4];  // C fragments: dimensions 64 g + 8 r + 2 t (c0 c1) and, 16-fold, the next one (c2 c3)
   float m[NT][2], l[NT][2], z[NT][NG][2];
-  float up[NT][NG][2];    // the power of two that p s is multiplied by
+  float up[NT][NG][2];    // the power of two, 2^-119 to 2^120, that p s is multiplied by
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -380,9 +381,12 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
       }
     }
   }
-  // p and, in f16, p s times its power of two. The maximum follows a logit that
-  // is more than 2^3 times above it (p up to 8 costs fp32 nothing), the power a p s of
-  // 2^15 or more: most steps change neither.
+  // p and, in f16, p s times its power of two. The maximum (rounded up to an
+  // integer) follows a logit that is more than 2^3 times above it (p up to 8 costs
+  // fp32 nothing), and the power rises by what the weights of the keys so far fall
+  // then, exactly: it looks back at no term that has lost its weight, and the sums
+  // in it stay as they are. The power follows a p s of 2^15 or more down: most steps
+  // change neither.
   float p[NT][KH][2];
   uint32_t ph[NT][NG][KH];
   auto weigh = [&]() {
@@ -422,23 +426,25 @@ __device__ __forceinline__ void q4_step(const uint8_t* st, int lane, int left, i
         float mn = S.m[j][i];
 #pragma unroll
         for (int h = 0; h < KH; ++h) mn = fmaxf(mn, sc[j][h][i]);
-        mn = column_max<FEW>(mn);
-        const float alpha = ex2(S.m[j][i] - mn);
+        mn = ceilf(column_max<FEW>(mn));
+        // The weights of the keys so far fall by 2^fall (below 2^-126: to nothing).
+        const int fall = -static_cast<int>(fmaxf(S.m[j][i] - mn, -252.f));
+        const float alpha = pow2_or_0(-fall);
         S.m[j][i] = mn;
         S.l[j][i] *= alpha;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           S.z[j][g][i] *= alpha;
-          float f = alpha, mx = 0.f;
+          float mx = 0.f;
 #pragma unroll
           for (int h = 0; h < KH; ++h)
             if (seen[j][h][i]) mx = fmaxf(mx, ex2(sc[j][h][i] - mn) * lo_f(vsz[g][h]));
           mx = column_max<FEW>(mx);
-          if (mx * S.up[j][g][i] >= 0x1p15f) {  // (the same in all lanes of the column)
-            const float up = pow2(min(9 - exponent(mx), 120));
-            f *= up * inverse_pow2(S.up[j][g][i]);
-            S.up[j][g][i] = up;
-          }
+          const int was = exponent(S.up[j][g][i]);
+          int now = min(was + fall, 120);
+          if (mx * pow2(now) >= 0x1p15f) now = min(9 - exponent(mx), 120);  // (the same in all lanes of the column)
+          S.up[j][g][i] = pow2(now);
+          const float f = pow2_or_0(now - was - fall);
 #pragma unroll
           for (int t = 0; t < 4; ++t) S.o[j][g][t][i] *= f, S.o[j][g][t][2 + i] *= f;
         }

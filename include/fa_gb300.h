@@ -460,7 +460,9 @@ int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_cod
  *                  workspaces of their own.
  * The values are z + s * code as they are, not rounded; logits, softmax and sums
  * are fp32, and p * s enters its product as f16 (after a power of two: 2^-11 of
- * each term). A row of q with elements of 2^114 or more may give NaN.
+ * each term down to 2^-23 of the largest p * s of the query and 64 elements, p
+ * being the softmax; 2^-34 of that for the smaller ones). A row of q with
+ * elements of 2^114 or more may give NaN.
  * Results are bitwise repeatable. Lengths and tables are checked on the host
  * only in check mode (FA_CHECK=1); otherwise lengths are clamped to
  * [0, max_seq_len] and block ids outside [0, num_blocks) read as zero keys and
