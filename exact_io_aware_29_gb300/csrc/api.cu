@@ -247,7 +247,7 @@ int check_decode_tables(const int* seq_lens, const int* table, int B, int max_bl
   if (e != cudaSuccess) return launch_error(e);
   for (int b = 0; b < B; ++b) {
     if (lens[b] < 0 || lens[b] > max_seq_len) return FA_ERR_INVALID;
-    for (int p = 0; p < (lens[b] + block_size - 1) / block_size; ++p) {
+    for (int p = 0; static_cast<long long>(p) * block_size < lens[b]; ++p) {
       const int x = tab[static_cast<size_t>(b) * max_blocks + p];
       if (x < 0 || x >= num_blocks) return FA_ERR_INVALID;
     }

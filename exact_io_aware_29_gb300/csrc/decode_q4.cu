@@ -116,7 +116,9 @@ constexpr float kNoLogit = -3.402823466e38f;  // the maximum before the first ke
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   return min(max(a.seq_lens[b], 0), a.max_seq_len);
 }
-__device__ __forceinline__ int q4_tiles(int L) { return (L + kQ4Tile - 1) / kQ4Tile; }
+__device__ __forceinline__ int q4_tiles(int L) {  // (L may be 2^31 - 1)
+  return static_cast<int>((static_cast<unsigned>(L) + kQ4Tile - 1) / kQ4Tile);
+}
 // How `total` units of work are shared out over `ctas` CTAs: runs of `per` or
 // per + 1, the longer ones first. A unit is a tile; an item may count as some
 // units more (its head), in front of its tiles.
@@ -531,9 +533,9 @@ struct Q4Copies {
     base = at;
     upto = min(at + 32 / C::HALVES, w.tile + w.here);
     const int tile = at + lane / C::HALVES;
-    const int key = tile * kQ4Tile + warp * C::KEYS + lane % C::HALVES * 16;
+    const int key = tile < upto ? tile * kQ4Tile + warp * C::KEYS + lane % C::HALVES * 16 : w.L;
     row = -1;
-    if (tile < upto && key < w.L) {
+    if (key < w.L) {
       const int block = key / a.block_size;
       const int phys = a.block_table[static_cast<long long>(w.b) * a.max_blocks + block];
       if (phys >= 0 && phys < a.num_blocks)

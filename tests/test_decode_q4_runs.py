@@ -146,3 +146,27 @@ def test_values_that_grow_with_their_weights():
             x.scales[0][page, :, slot, 0, 1] += (7.0 * (tile - 15) * math.log(2) / (51 * x.scale)).to(torch.bfloat16)
             x.scales[1][page, :, slot] *= torch.exp2(float(fall) * (15 - tile))[..., None, None].to(torch.bfloat16)
         x.check(*x.run())
+
+
+def test_the_longest_sequence():
+    """2^31 - 1 tokens (pages of the same block over and over): every logit 0,
+    so that the sums of a warp's keys are whole numbers, and every value 1. The
+    block of the last page reads as NaN in the slot behind the last token."""
+    import torch
+    page, lens = 65536, [2 ** 31 - 1, 100]
+    codes = torch.randint(0, 256, (2, 1, page, 32), dtype=torch.uint8, device="cuda")
+    k_scales, v_scales = (torch.zeros(2, 1, page, 1, 2, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    v_scales[..., 1] = 1.0
+    k_scales[1, :, -1], v_scales[1, :, -1] = float("nan"), float("nan")
+    table = torch.zeros(2, 2 ** 31 // page, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    q = torch.randn(2, 1, 64, device="cuda").to(torch.bfloat16)
+    o, lse = binding.attention_decode_paged_q4(q, codes, k_scales, codes, v_scales, table,
+                                               torch.tensor(lens, dtype=torch.int32, device="cuda"), 2 ** 31 - 1, 0.1)
+    torch.cuda.synchronize()
+    assert binding.fa_check_status() == binding.FA_OK
+    assert bool((o == 1).all())
+    # The parts' sums in base 2, joined in fp32 over at most 608 CTAs.
+    for b, L in enumerate(lens):
+        ref = math.log(L)
+        assert abs(float(lse[b]) - ref) <= 2.0 ** -21 * (1 + ref) + 608 * 2.0 ** -24
