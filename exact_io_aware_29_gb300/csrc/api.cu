@@ -351,6 +351,7 @@ int check_gather_tables(const int* table, const int* starts, const int* cu, int 
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return launch_error(e);
   for (int b = 0; b < batch; ++b) {
+    if (at[b + 1] == at[b]) continue;  // of a sequence without rows nothing is read
     const long long end = static_cast<long long>(first[b]) + at[b + 1] - at[b];
     if (first[b] < 0 || end > static_cast<long long>(max_blocks) * block_size) return FA_ERR_INVALID;
     for (long long p = first[b] / block_size; p * block_size < end; ++p) {

@@ -161,3 +161,30 @@ def test_contracts_are_checked_on_the_host():
     r = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, env={**os.environ, "FA_CHECK": "1"}, text=True,
                        capture_output=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+EMPTY_CHILD = r"""
+import torch
+from exact_io_aware_29_gb300 import binding as fa
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+q4 = fa.kv_cache_q4(3, 2, 16, 64)
+for starts in (5, 16, 32, 33, 2 ** 31 - 1, -1):
+    # The first sequence has no rows: neither its start nor its pages are looked at.
+    k, v = fa.kv_gather_q4(*q4, i32(-1, 99, 1, 0).view(2, 2), i32(starts, 3), i32(0, 0, 20), 20)
+    assert not k.any() and not v.any()
+try:
+    fa.kv_gather_q4(*q4, i32(-1, 99, 1, 0).view(2, 2), i32(5, 3), i32(0, 1, 20), 20)
+except fa.FaError as e:
+    assert e.status == fa.FA_ERR_INVALID
+    print("done")
+"""
+
+
+@pytest.mark.gpu
+def test_a_gather_of_no_row_reads_no_page():
+    r = subprocess.run([sys.executable, "-c", EMPTY_CHILD], cwd=ROOT, env={**os.environ, "FA_CHECK": "1"}, text=True,
+                       capture_output=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
