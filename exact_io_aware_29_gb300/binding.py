@@ -783,9 +783,10 @@ def fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, i
 
 
 def kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, interleaved: bool = False, stream=None):
-    """Allocates the rotated queries [T, H, d], then calls fa_kv_append. Returns them."""
+    """Allocates the rotated queries [T, H, d], then calls fa_kv_append. Returns
+    them (None if q is None)."""
     torch = _load_torch()
-    q_out = _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    q_out = None if q is None else _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     fa_kv_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, interleaved, stream)
     return q_out
 
@@ -832,9 +833,10 @@ def fa_kv_append_q4(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scale
 
 def kv_append_q4(q, k, v, cos, sin, positions, slots, k_codes, k_scales, v_codes, v_scales,
                  interleaved: bool = False, stream=None):
-    """Allocates the rotated queries [T, H, d], then calls fa_kv_append_q4. Returns them."""
+    """Allocates the rotated queries [T, H, d], then calls fa_kv_append_q4.
+    Returns them (None if q is None)."""
     torch = _load_torch()
-    q_out = _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
+    q_out = None if q is None else _alloc(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     fa_kv_append_q4(q, k, v, cos, sin, positions, slots, q_out, k_codes, k_scales, v_codes, v_scales, interleaved,
                     stream)
     return q_out

@@ -188,3 +188,27 @@ def test_a_gather_of_no_row_reads_no_page():
     r = subprocess.run([sys.executable, "-c", EMPTY_CHILD], cwd=ROOT, env={**os.environ, "FA_CHECK": "1"}, text=True,
                        capture_output=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("name", ["kv_append", "kv_append_q4"])
+def test_without_queries_host_tensors_are_refused_like_others(name):
+    x = {k: t for k, t in calls("cpu")["fa_" + name][1].items() if k != "q_out"}
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(binding, name)(**{**x, "q": None})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["kv_append", "kv_append_q4"])
+def test_the_forms_that_allocate_take_no_queries_too(name):
+    import torch
+    x = {k: t for k, t in calls("cuda")["fa_" + name][1].items() if k != "q_out"}
+    caches = [k for k in x if k.startswith(("k_", "v_"))]
+    for k in ("k", "v"):
+        x[k].normal_()
+    q = getattr(binding, name)(**x)
+    want = [x[c].clone() for c in caches]
+    assert q.shape == x["q"].shape and any(t.any() for t in want)
+    for c in caches:
+        x[c].zero_()
+    assert getattr(binding, name)(**{**x, "q": None}) is None
+    assert all(torch.equal(x[c], w) for c, w in zip(caches, want))
