@@ -5,6 +5,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <unordered_map>
 #include <vector>
@@ -155,6 +156,19 @@ bool encode_u8(CUtensorMap* m, const void* ptr, long long dim0, long long dim1, 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Check mode: n integers of the device, on the host. No exception passes a C
+// entry: sizes that the host has no memory for are unsupported.
+int to_host(std::vector<int>* h, const int* src, long long n, cudaStream_t stream) {
+  try {
+    h->resize(static_cast<size_t>(n));
+  } catch (const std::exception&) {
+    return FA_ERR_UNSUPPORTED;
+  }
+  cudaError_t e = cudaMemcpyAsync(h->data(), src, sizeof(int) * h->size(), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? static_cast<int>(FA_OK) : launch_error(e);
+}
+
 // Check mode: copy cu_seqlens to the host and validate them (`spare`: rows of
 // no sequence may follow the last one).
 int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream, bool spare = false);
@@ -180,10 +194,9 @@ int check_shape(int B, int H, int N, int d, float scale) {
 // Check mode: copy kv_lens to the host and validate them.
 int check_kv_lens(const int* kv_lens, int B, int N, cudaStream_t stream) {
   if (kv_lens == nullptr || !check_mode()) return FA_OK;
-  std::vector<int> h(B);
-  cudaError_t e = cudaMemcpyAsync(h.data(), kv_lens, sizeof(int) * B, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> h;
+  const int st = to_host(&h, kv_lens, B, stream);
+  if (st != FA_OK) return st;
   for (int b = 0; b < B; ++b)
     if (h[b] < 0 || h[b] > N) return FA_ERR_INVALID;
   return FA_OK;
@@ -191,10 +204,9 @@ int check_kv_lens(const int* kv_lens, int B, int N, cudaStream_t stream) {
 
 int check_cu_seqlens(const int* cu, int batch, int total, int max_len, cudaStream_t stream, bool spare) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> h(batch + 1);
-  cudaError_t e = cudaMemcpyAsync(h.data(), cu, sizeof(int) * (batch + 1), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> h;
+  const int st = to_host(&h, cu, batch + 1LL, stream);
+  if (st != FA_OK) return st;
   if (h[0] != 0 || (spare ? h[batch] > total : h[batch] != total)) return FA_ERR_INVALID;
   for (int b = 0; b < batch; ++b)
     if (h[b + 1] < h[b] || h[b + 1] - h[b] > max_len) return FA_ERR_INVALID;
@@ -239,12 +251,10 @@ DecodePlan decode_plan(int B, int H, int max_seq_len) {
 int check_decode_tables(const int* seq_lens, const int* table, int B, int max_blocks, int block_size,
                         int num_blocks, int max_seq_len, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> lens(B), tab(static_cast<size_t>(B) * max_blocks);
-  cudaError_t e = cudaMemcpyAsync(lens.data(), seq_lens, sizeof(int) * B, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyAsync(tab.data(), table, sizeof(int) * tab.size(), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> lens, tab;
+  int st = to_host(&tab, table, static_cast<long long>(B) * max_blocks, stream);
+  if (st == FA_OK) st = to_host(&lens, seq_lens, B, stream);
+  if (st != FA_OK) return st;
   for (int b = 0; b < B; ++b) {
     if (lens[b] < 0 || lens[b] > max_seq_len) return FA_ERR_INVALID;
     for (int p = 0; static_cast<long long>(p) * block_size < lens[b]; ++p) {
@@ -311,15 +321,14 @@ void shared_plan(fa::SharedArgs* a) {
 // Check mode: the tables and lengths of a shared-prefix step on the host.
 int check_shared_tables(const fa::SharedArgs& a, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> cu(a.P + 1);
-  cudaError_t e = cudaMemcpyAsync(cu.data(), a.cu_seqs, sizeof(int) * cu.size(), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> cu;
+  int st = to_host(&cu, a.cu_seqs, a.P + 1LL, stream);
+  if (st != FA_OK) return st;
   if (cu[0] < 0 || cu[a.P] > a.B) return FA_ERR_INVALID;
   for (int p = 0; p < a.P; ++p)
     if (cu[p + 1] < cu[p] || cu[p + 1] - cu[p] > a.max_group) return FA_ERR_INVALID;
-  const int st = check_decode_tables(a.prefix_lens, a.prefix_table, a.P, a.max_prefix_blocks, a.block_size,
-                                     a.num_blocks, a.max_prefix_len, stream);
+  st = check_decode_tables(a.prefix_lens, a.prefix_table, a.P, a.max_prefix_blocks, a.block_size,
+                           a.num_blocks, a.max_prefix_len, stream);
   if (st != FA_OK) return st;
   return check_decode_tables(a.seq_lens, a.block_table, a.B, a.max_blocks, a.block_size, a.num_blocks, a.max_seq_len,
                              stream);
@@ -328,10 +337,9 @@ int check_shared_tables(const fa::SharedArgs& a, cudaStream_t stream) {
 // Check mode: the slots of an append are the pool's or negative, and no two alike.
 int check_slots(const int* slots, int T, long long pool, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> h(T);
-  cudaError_t e = cudaMemcpyAsync(h.data(), slots, sizeof(int) * T, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> h;
+  const int st = to_host(&h, slots, T, stream);
+  if (st != FA_OK) return st;
   std::sort(h.begin(), h.end());
   for (int i = 0; i < T; ++i)
     if (h[i] >= pool || (i > 0 && h[i] >= 0 && h[i] == h[i - 1])) return FA_ERR_INVALID;
@@ -342,19 +350,17 @@ int check_slots(const int* slots, int T, long long pool, cudaStream_t stream) {
 int check_gather_tables(const int* table, const int* starts, const int* cu, int batch, int max_blocks, int block_size,
                         int num_blocks, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> tab(static_cast<size_t>(batch) * max_blocks), first(batch, 0), at(batch + 1);
-  cudaError_t e = cudaMemcpyAsync(tab.data(), table, sizeof(int) * tab.size(), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess && starts != nullptr)
-    e = cudaMemcpyAsync(first.data(), starts, sizeof(int) * batch, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyAsync(at.data(), cu, sizeof(int) * at.size(), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> tab, first, at;
+  int st = to_host(&tab, table, static_cast<long long>(batch) * max_blocks, stream);
+  if (st == FA_OK && starts != nullptr) st = to_host(&first, starts, batch, stream);
+  if (st == FA_OK) st = to_host(&at, cu, batch + 1LL, stream);
+  if (st != FA_OK) return st;
   for (int b = 0; b < batch; ++b) {
     if (at[b + 1] == at[b]) continue;  // of a sequence without rows nothing is read
-    const long long end = static_cast<long long>(first[b]) + at[b + 1] - at[b];
-    if (first[b] < 0 || end > static_cast<long long>(max_blocks) * block_size) return FA_ERR_INVALID;
-    for (long long p = first[b] / block_size; p * block_size < end; ++p) {
+    const int start = starts != nullptr ? first[b] : 0;
+    const long long end = static_cast<long long>(start) + at[b + 1] - at[b];
+    if (start < 0 || end > static_cast<long long>(max_blocks) * block_size) return FA_ERR_INVALID;
+    for (long long p = start / block_size; p * block_size < end; ++p) {
       const int x = tab[static_cast<size_t>(b) * max_blocks + p];
       if (x < 0 || x >= num_blocks) return FA_ERR_INVALID;
     }
@@ -1114,10 +1120,9 @@ static int norm_rope_args(fa::NormRopeArgs* a, const void* q, const void* k, con
 // Check mode: copy the positions to the host and validate them.
 static int check_positions(const int* positions, int T, int max_pos, cudaStream_t stream) {
   if (!check_mode()) return FA_OK;
-  std::vector<int> h(T);
-  cudaError_t e = cudaMemcpyAsync(h.data(), positions, sizeof(int) * T, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return launch_error(e);
+  std::vector<int> h;
+  const int st = to_host(&h, positions, T, stream);
+  if (st != FA_OK) return st;
   for (int p : h)
     if (p < 0 || p >= max_pos) return FA_ERR_INVALID;
   return FA_OK;

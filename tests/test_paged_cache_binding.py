@@ -212,3 +212,22 @@ def test_the_forms_that_allocate_take_no_queries_too(name):
         x[c].zero_()
     assert getattr(binding, name)(**{**x, "q": None}) is None
     assert all(torch.equal(x[c], w) for c, w in zip(caches, want))
+
+
+HUGE_CHILD = r"""
+from exact_io_aware_29_gb300 import binding as fa
+
+lib, x = fa.load_library(), 0x10000  # (nothing is read: the tables' copies come first, and there is no room for them)
+for blocks in (1 << 30, 2 ** 31 - 1):  # tables of 2^50 entries and more
+    st = [lib.fa_decode_paged_q4(*[x] * 9, 1 << 20, 1, 1, 1, 64, 10, 16, blocks, 64, 0.1, x, 1 << 60, None),
+          lib.fa_decode_paged(*[x] * 7, 1 << 20, 1, 64, 10, 64, blocks, 64, 0.1, x, 1 << 60, None)]
+    assert st == [fa.FA_ERR_UNSUPPORTED] * 2, st
+print("done")
+"""
+
+
+def test_tables_that_the_host_has_no_room_for_are_refused():
+    """Check mode copies them; no exception leaves a C entry."""
+    r = subprocess.run([sys.executable, "-c", HUGE_CHILD], cwd=ROOT, env={**os.environ, "FA_CHECK": "1"}, text=True,
+                       capture_output=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
