@@ -231,3 +231,10 @@ def test_tables_that_the_host_has_no_room_for_are_refused():
     r = subprocess.run([sys.executable, "-c", HUGE_CHILD], cwd=ROOT, env={**os.environ, "FA_CHECK": "1"}, text=True,
                        capture_output=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("name", [*NAMES, "kv_append", "kv_append_q4", "kv_cache_q4", "kv_gather_q4",
+                                  "attention_decode_paged_q4", "fa_decode_paged_q4_workspace_size"])
+def test_the_package_exports_them(name):
+    import exact_io_aware_29_gb300 as package
+    assert getattr(package, name) is getattr(binding, name)
