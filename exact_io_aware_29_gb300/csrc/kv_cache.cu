@@ -326,7 +326,9 @@ static cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
   // bf16; written in 4 bits and read back, 138, 115, 82 and 78 us, 16 + 4 heads
   // 73, 61, 46 and 50; 512 tokens of those 5.9, 5.8, 6.7 and 6.8.)
   const long long lanes = a.T * (a.H + 2 * a.Hk) * (D / 8);
-  if (Q4 && D == 128 && a.Hk >= 8 && lanes >= 152LL * 4 * 256 * 8) return launch_append_r<D, Q4, 8>(a, stream);
+  if constexpr (Q4 && D == 128) {
+    if (a.Hk >= 8 && lanes >= 152LL * 4 * 256 * 8) return launch_append_r<D, Q4, 8>(a, stream);
+  }
   return lanes >= 152LL * 2 * 256 * 4 ? launch_append_r<D, Q4, 4>(a, stream) : launch_append_r<D, Q4, 1>(a, stream);
 }
 
