@@ -170,3 +170,20 @@ def test_the_longest_sequence():
     for b, L in enumerate(lens):
         ref = math.log(L)
         assert abs(float(lse[b]) - ref) <= 2.0 ** -21 * (1 + ref) + 608 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("d,n,H", [(64, 1, 8), (64, 3, 24), (128, 1, 32), (128, 5, 24)])
+def test_runs_of_many_tiles(d, n, H):
+    """Ragged sequences, empty ones among them, of enough tiles that an item
+    counts as some tiles more in the shares: runs that begin and end anywhere,
+    before the first tile of an item too, whole items between them."""
+    import random
+    rng = random.Random(d + n)
+    lens = [rng.choice([0, rng.randint(1, 300), rng.randint(1000, 9000), rng.randint(5000, 9000)]) for _ in range(96)]
+    x = Step(lens, n, H, 8, d, 64, 8950 + d + n, bound=20000)
+    ctas = 152 * ((4 if d == 64 else 3) - (n * H // 8 > 8))
+    assert sum(-(-L // 128) for L in lens) * 8 >= 8 * ctas
+    o, lse = x.run()
+    x.check(o, lse)
+    again = x.run()
+    assert bool((o == again[0]).all()) and bool((lse == again[1]).all())
