@@ -312,6 +312,29 @@ def test_caches_past_2_31_bytes_and_elements(q4):
 
 
 @pytest.mark.gpu
+def test_4_bit_cache_past_2_31_words():
+    """Slots whose codes lie more than 2^31 32-bit words (2^33 bytes, 2^34
+    codes) into a 4-bit cache, written and read back."""
+    import torch
+    Hk, d, page, blocks = 8, 128, 256, 70000
+    x = Append(300, 8, Hk, d, 128, page, 9810)
+    assert (blocks - x.blocks) * Hk * page * d // 8 > 2 ** 31
+    cache, want = (binding.kv_cache_q4(n, Hk, page, d) for n in (blocks, x.blocks))
+    binding.kv_append_q4(*x.args()[:-1], x.dev[1] + (blocks - x.blocks) * page, *cache)
+    binding.kv_append_q4(*x.args(), *want)
+    assert all(torch.equal(t[blocks - x.blocks:], w) for t, w in zip(cache, want))
+    for t in cache:
+        for part in t[:blocks - x.blocks].split(10000):
+            assert not part.any()
+    cu = torch.tensor([0, x.blocks * page], dtype=torch.int32, device="cuda")
+    table = torch.arange(x.blocks, dtype=torch.int32, device="cuda").view(1, -1)
+    got = binding.kv_gather_q4(*cache, table + (blocks - x.blocks), None, cu, x.blocks * page)
+    ref = binding.kv_gather_q4(*want, table, None, cu, x.blocks * page)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and all(t.any() for t in ref)
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     """Captured appends and gathers replayed on new tokens and slots, while the
     same calls run eagerly on a second stream on another cache."""
