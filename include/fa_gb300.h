@@ -394,8 +394,8 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* q_weight, cons
  *   k_cache, v_cache  device bf16 [num_blocks, block_size, H_kv, d]; other slots
  *                  are left as they were.
  *   rot            a multiple of 16 in [0, d]; d in {64, 128}.
- * Errors as for fa_qk_norm_rope; FA_ERR_UNSUPPORTED also for a pool of 2^31 or
- * more slots.
+ * Errors as for fa_qk_norm_rope (T = 0 is FA_ERR_INVALID: there is no empty
+ * call); FA_ERR_UNSUPPORTED also for a pool of 2^31 or more slots.
  */
 int fa_kv_append(const void* q, const void* k, const void* v, const float* cos, const float* sin,
                  const int* positions, const int* slots, void* q_out, void* k_cache, void* v_cache, int T, int H,
@@ -406,7 +406,8 @@ int fa_kv_append(const void* q, const void* k, const void* v, const float* cos, 
  * The same for a cache held in 4 bits (4.5 with the scales): 64 consecutive
  * elements x of a key or value row (as fa_kv_append would store it) become
  *   z = min x,  s = bf16((max x - min x) / 15) (0 below 2^-126),
- *   code = (x - z) / s to the nearest integer, ties to even, in 0..15 (0 if s = 0)
+ *   code = (x - z) / s to the nearest integer, ties to even, in 0..15 (0 if s = 0;
+ *          x - z rounded to fp32 if the two are more than 2^16 apart)
  * and stand for z + s * code. A group with a NaN or an infinity, or whose range
  * is past fp32, reads as NaN (s = z = NaN, codes 0).
  *   k_codes, v_codes    device uint8 [num_blocks, H_kv, block_size, d / 2]: byte
@@ -433,8 +434,9 @@ int fa_kv_append_q4(const void* q, const void* k, const void* v, const float* co
  *                  total_k.
  *   k, v           device bf16 [total_k, H_kv, d]. Rows of no sequence are left
  *                  as they were.
- * Check mode validates offsets, starts and tables on the host; otherwise tokens
- * outside the table's row and blocks outside the pool read as zeros.
+ * Check mode validates offsets, starts and tables on the host (neither the start
+ * nor the pages of a sequence without rows); otherwise tokens outside the table's
+ * row and blocks outside the pool read as zeros. total_k = 0 is FA_ERR_INVALID.
  */
 int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
                     const int* block_table, const int* starts, const int* cu_seqlens_k, void* k, void* v, int batch,
@@ -450,7 +452,8 @@ int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_cod
  * prompt behind a long context.
  *   q, o           device bf16 [B, n_new, H, d];  lse  device fp32 [B, n_new, H]
  *                  (natural log; -inf and O = 0 for a query that sees no token,
- *                  and for nothing else: a NaN logit gives NaN in both).
+ *                  or whose logits all overflow to -inf, and for nothing else: a
+ *                  logit that is NaN or +inf gives NaN in both).
  *   block_table    device int32 [B, max_blocks_per_seq];  seq_lens device int32
  *                  [B], each in [0, max_seq_len]. Entries past a sequence's last
  *                  page are not read; slots past its length may hold anything.
@@ -462,7 +465,8 @@ int fa_kv_gather_q4(const void* k_codes, const void* k_scales, const void* v_cod
  * are fp32, and p * s enters its product as f16 (after a power of two: 2^-11 of
  * each term down to 2^-23 of the largest p * s of the query and 64 elements, p
  * being the softmax; 2^-34 of that for the smaller ones). A row of q with
- * elements of 2^114 or more may give NaN.
+ * elements of 2^114 or more may give NaN; sums of p * value are divided last, so
+ * values whose size times the number of tokens passes 2^124 may give infinities.
  * Results are bitwise repeatable. Lengths and tables are checked on the host
  * only in check mode (FA_CHECK=1); otherwise lengths are clamped to
  * [0, max_seq_len] and block ids outside [0, num_blocks) read as zero keys and
@@ -494,7 +498,8 @@ const char* fa_last_cuda_error(void);
  * kind 0 = forward, 1 = backward pre-pass, 2 = backward main kernel,
  * 3 = backward dQ conversion. (The grouped-head forms count as the kernels they
  * are compiled from; a shared-prefix decoding step records its tensor-core
- * prefix part as kind 0, its streamed part as 4 and the joining kernel as 5.)
+ * prefix part as kind 0, its streamed part as 4 and the joining kernel as 5; a
+ * step over a 4-bit cache counts as 4, its joining kernel, if it has one, as 5.)
  * fa_timing_end() releases the events; calls made
  * after n launches of a kind are no longer timed. Returns fa_status.
  */

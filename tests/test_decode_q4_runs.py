@@ -187,3 +187,28 @@ def test_runs_of_many_tiles(d, n, H):
     x.check(o, lse)
     again = x.run()
     assert bool((o == again[0]).all()) and bool((lse == again[1]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 4])
+@pytest.mark.parametrize("bound", [0, 20000])
+def test_logits_past_fp32(d, n, bound):
+    """Where every logit overflows to -inf, O is 0 and the LSE -inf; where one
+    is +inf, both are NaN; the other sequence keeps its bits."""
+    import torch
+    x = Step([500, 300], n, 8, 2, d, 64, 8990 + d + n, bound=bound)
+    o, lse = x.run()
+    page, slot = x.place(0)
+    x.q[0] = x.q[0].abs() * 2.0 ** 40
+    x.q[0, :, ::2] *= -1
+    for count in (500, 128):  # the keys whose minimum lies far below zero: all of them, the first tile's
+        if count < 500:
+            x.scales[0][page, :, slot, :, 1] = 0.0
+        x.scales[0][page[:count], :, slot[:count], :, 1] = -2.0 ** 125
+        o1, l1 = x.run()
+        assert torch.equal(o1[1], o[1]) and torch.equal(l1[1], lse[1])
+        assert bool(o1[0, :, ::2].isnan().all()) and bool(l1[0, :, ::2].isnan().all())
+        if count == 500:
+            assert not o1[0, :, 1::2].any() and bool((l1[0, :, 1::2] == NEG).all())
+        else:
+            assert bool(o1[0, :, 1::2].isfinite().all()) and bool(l1[0, :, 1::2].isfinite().all())
