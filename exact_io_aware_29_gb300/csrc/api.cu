@@ -1347,12 +1347,12 @@ static int q4_sizes(fa::Q4DecodeArgs* a, int B, int n_new, int H, int H_kv, int 
   // A cluster for each item, as many CTAs as leave room for all clusters at once
   // and have a tile each, unless a CTA would have many tiles to go through, or
   // more than the shares of an even split. (32/8 heads, d 128, in us, split evenly
-  // and in clusters of 8, 4, 2 and 1: one sequence of 1000 tokens 7.7, 6.6, 7.0,
-  // 8.1, 9.5; 8 of 3000 13.7, 17.8, 11.4, 13.5, 20; 16 of 3000 22.7, 30, 24, 17.4,
-  // 21; 48 of 1000 22, 57, 35, 24, 17.4; 256 of 1000 66, 276, 150, 95, 67. One of
-  // 30000 17.3, 25; 16 of 8000 32.3, 44, 38, 33.5; 80 of 3000 54, 116, 75, 60, 58;
-  // with one key head, 1, 4 and 16 of 8000 8.7, 10.0 and 15.7, in clusters of 8
-  // 10.7, 11.1 and 13.7.)
+  // and in clusters of 8, 4, 2 and 1: one sequence of 1000 tokens 7.6, 6.4, 6.7,
+  // 7.7, 9.1; 8 of 3000 15.2, 19, 12.2, 13.8, 20; 16 of 3000 22, 29, 24, 16.9, 20;
+  // 48 of 1000 21, 55, 34, 23, 16.7; 256 of 1000 64, 266, 146, 93, 65. One of 30000
+  // 17.2, 24; 16 of 8000 31.8, 43, 39, 32.0; 80 of 3000 53, 112, 73, 59, 56; with
+  // one key head, 1, 4 and 16 of 8000 8.1, 9.4 and 16.1, in clusters of 8 9.8, 9.9
+  // and 12.7.)
   int cs = fa::kQ4Cluster;
   while (cs > 1 && (items * cs > ctas || cs / 2 >= tiles)) cs /= 2;
   const int most = cs == 1 ? 8 : (items * cs * 2 > ctas ? 16 : (items >= 8 ? 8 : 6));

@@ -20,9 +20,11 @@
 //   P V: p s is scaled by a power of two of the row and group, such that the
 //   largest so far, each at its present weight, lies in [2^9, 2^15): rounded to
 //   f16, 2^-11 of a term (an eighth of what the rounding of O to bf16 costs), at
-//   terms down to 2^-23 of the largest (and 2^-134). (As the sum of two bf16
-//   numbers, whose exponents need no care, it takes twice the products and a
-//   third more instructions.)
+//   terms down to 2^-23 of the largest (and 2^-134). It is a choice for speed:
+//   as the sum of two f16 numbers, 64 sequences of 1024 to 8192 tokens, 32/8
+//   heads, d 128, take 65.1 us instead of 59.5, with four drafts each 113 instead
+//   of 96, and O is off by 1.67e-3 instead of 1.74e-3 (its rounding to bf16 alone:
+//   1.665e-3).
 // The logic pipe, not the tensor cores, stands nearest to HBM: about 125
 // instructions on it for 16 keys, of 205 that HBM leaves time for (d 128).
 //
@@ -38,7 +40,7 @@
 // A step of few, short sequences goes another way, its time being a sum of
 // latencies: a cluster of up to eight CTAs shares an item's tiles and joins its
 // parts through their shared memory.
-// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 60.0 us, 5.5 TB/s (the
+// 64 sequences of 1024 to 8192 tokens, 32/8 heads, d 128: 59.5 us, 5.6 TB/s (the
 // copies alone 59); one of 131072: 32.7 us, 4.6 TB/s. About 8 of them are spent
 // before the first tile and after the last.
 #include <cuda_bf16.h>
@@ -56,7 +58,7 @@ struct Q4Cfg {
   static constexpr int HALVES = KEYS / 16;
   static constexpr int WARPS = kQ4Tile / KEYS;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int CTAS = q4_ctas(D, ROWS);    // per SM (registers: 168, 128 at d 64 with NT = 1)
+  static constexpr int CTAS = q4_ctas(D, ROWS);    // per SM (registers at most: 168; at d 64 with NT = 1 128, at d 128 with NT = 2 255)
   // A stage of a warp's ring: codes of K and V, scales of K and V.
   static constexpr int CODE_BYTES = KEYS * D / 2, SCALE_BYTES = KEYS * NG * 4;
   static constexpr int OFF_VC = CODE_BYTES, OFF_KS = 2 * CODE_BYTES, OFF_VS = OFF_KS + SCALE_BYTES;
@@ -614,9 +616,9 @@ __device__ __forceinline__ Q4Start q4_start(const Q4DecodeArgs& a, uint8_t* smem
   }
   // An item costs about three tiles' time besides its tiles (its queries, the
   // first steps' maxima, the join of the warps), six with 9 to 16 rows: 64
-  // sequences of up to 8192 tokens 60.0 us, 70 if it is left out, and 101 with
-  // four drafts each, 111 if it counts as three. Where runs are short, what counts
-  // is the longest of them: only tiles then.
+  // sequences of up to 8192 tokens 59.5 us, 70 if it is left out, and 96 with four
+  // drafts each, 104 if it counts as three. Where runs are short, what counts is
+  // the longest of them: only tiles then.
   const int tiles = static_cast<int>(all) * items;
   const int cta = blockIdx.x, ctas = min(static_cast<int>(gridDim.x), tiles);  // one tile each at least
   const int head = tiles >= 8 * ctas ? q4_head(C::ROWS) : 0;
