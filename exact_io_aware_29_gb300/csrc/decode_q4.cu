@@ -58,7 +58,8 @@ struct Q4Cfg {
   static constexpr int HALVES = KEYS / 16;
   static constexpr int WARPS = kQ4Tile / KEYS;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int CTAS = q4_ctas(D, ROWS);    // per SM (registers at most: 168; at d 64 with NT = 1 128, at d 128 with NT = 2 255)
+  // Per SM; registers at most 168, 128 at d 64 with NT = 1, 255 at d 128 with NT = 2.
+  static constexpr int CTAS = q4_ctas(D, ROWS);
   // A stage of a warp's ring: codes of K and V, scales of K and V.
   static constexpr int CODE_BYTES = KEYS * D / 2, SCALE_BYTES = KEYS * NG * 4;
   static constexpr int OFF_VC = CODE_BYTES, OFF_KS = 2 * CODE_BYTES, OFF_VS = OFF_KS + SCALE_BYTES;
